@@ -52,7 +52,7 @@ typedef enum gdn_status {
 
 typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 
-typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
+typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_SIGMOID = 2 } gdn_activation;
 
 /* flags */
 #define GDN_FLAG_L2NORM_QK 1u /* L2-normalise q and k per head (eps 1e-6 inside the sqrt) */
@@ -449,6 +449,121 @@ typedef struct gdn_conv1d_backward_args {
 size_t gdn_conv1d_backward_workspace_size(const gdn_conv1d_backward_args* args);
 
 gdn_status gdn_conv1d_backward(const gdn_conv1d_backward_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * gdn_rms_norm -- RMS norm of rows, fused with what stands before and after a
+ * block: the residual sum and its scale, and the output gate (the mixer's
+ * output o is normed per head and gated with SiLU(z) before its projection).
+ *
+ *   GDN_NORM_PRE   h = residual + scale x,  y = h r (weight + weight_offset) act(gate)
+ *   GDN_NORM_POST  y = residual + scale x r (weight + weight_offset) act(gate)
+ *   r = 1 / sqrt(mean(h^2) + eps) over a row's `width` elements (of x in the
+ *   post order).  Sums and products are fp32; each output is rounded once (in
+ *   the pre order y is formed from the unrounded h).
+ *
+ *   dtype        GDN_BF16 or GDN_F32: dtype of x, gate, residual, y and sum.
+ *   weight_dtype dtype of weight (GDN_BF16 or GDN_F32).
+ *   order        GDN_NORM_PRE or GDN_NORM_POST.
+ *   activation   of the gate: GDN_ACT_SILU or GDN_ACT_SIGMOID (ignored
+ *                without a gate).
+ *   tokens       >= 0;  heads >= 1: rows of one token lie side by side
+ *                (tokens * heads < 2^31);  width 1..16384.
+ *   x, gate, residual, y, sum
+ *                [tokens, heads, width], token strides x_stride, ... in
+ *                elements (heads contiguous inside a token).  16-byte loads
+ *                are used where every pointer and stride allows them; any
+ *                element-aligned layout is valid.
+ *   weight       [width], or NULL for ones (weight_offset is then unused).
+ *   gate         or NULL: no gate.
+ *   residual     or NULL: no residual (the pre order then needs scale = 1).
+ *   sum          the pre order's h; required with a residual in the pre
+ *                order, NULL otherwise.
+ * y and sum may be one of the inputs itself (same pointer and stride); any
+ * other overlap of an output is refused.
+ * ---------------------------------------------------------------------- */
+typedef enum gdn_norm_order { GDN_NORM_PRE = 0, GDN_NORM_POST = 1 } gdn_norm_order;
+
+typedef struct gdn_rms_norm_args {
+  uint32_t struct_size;
+  int32_t dtype;
+  int32_t weight_dtype;
+  int32_t order;
+  int32_t activation;
+  int32_t heads;
+  int32_t width;
+  float eps;
+  float scale;
+  float weight_offset;
+  int64_t tokens;
+  const void* x;
+  const void* weight;
+  const void* gate;
+  const void* residual;
+  void* y;
+  void* sum;
+  int64_t x_stride;
+  int64_t gate_stride;
+  int64_t residual_stride;
+  int64_t y_stride;
+  int64_t sum_stride;
+} gdn_rms_norm_args;
+
+gdn_status gdn_rms_norm(const gdn_rms_norm_args* args, void* stream);
+
+/* gdn_rms_norm_backward -- gradients of gdn_rms_norm.
+ *   x            what was normed: the forward call's x, or its `sum` where
+ *                the pre order had a residual.
+ *   dy           gradient of y.
+ *   d_sum        gradient that reaches the forward call's `sum` from its
+ *                other uses, or NULL (pre order only).
+ *   dx           gradient of the forward call's x (scale times that of the
+ *                sum in the pre order), or NULL (not written).
+ *   d_residual   pre order: gradient of the sum, and so of the residual, or
+ *                NULL.  In the post order the residual's gradient is dy
+ *                itself: NULL.
+ *   dgate        gradient of the gate (required with one).
+ *   dweight      [width] fp32, or NULL (not formed).
+ *   workspace    gdn_rms_norm_backward_workspace_size() bytes, 256-byte
+ *                aligned, when dweight is asked for: partial rows, added in a
+ *                fixed order.
+ * The other fields are as in the forward call.  An output may be one of the
+ * row inputs itself (same pointer and stride). */
+typedef struct gdn_rms_norm_backward_args {
+  uint32_t struct_size;
+  int32_t dtype;
+  int32_t weight_dtype;
+  int32_t order;
+  int32_t activation;
+  int32_t heads;
+  int32_t width;
+  float eps;
+  float scale;
+  float weight_offset;
+  int64_t tokens;
+  const void* x;
+  const void* weight;
+  const void* gate;
+  const void* dy;
+  const void* d_sum;
+  void* dx;
+  void* d_residual;
+  void* dgate;
+  float* dweight;
+  int64_t x_stride;
+  int64_t gate_stride;
+  int64_t dy_stride;
+  int64_t d_sum_stride;
+  int64_t dx_stride;
+  int64_t d_residual_stride;
+  int64_t dgate_stride;
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_rms_norm_backward_args;
+
+/* Reads tokens, heads and width; 0 when they are invalid. */
+size_t gdn_rms_norm_backward_workspace_size(const gdn_rms_norm_backward_args* args);
+
+gdn_status gdn_rms_norm_backward(const gdn_rms_norm_backward_args* args, void* stream);
 
 /* Diagnostics. */
 const char* gdn_status_string(gdn_status status);

@@ -12,7 +12,8 @@ Entry points (same names as the C ABI):
     decode_step  one token per sequence: conv step + recurrence, state in place
     prefill_backward, conv1d_backward   gradients of prefill and conv1d
 and gdn_layer / gdn_layer_backward, which chain them for a whole token mixer
-layer.
+layer.  Around the mixer in a hybrid block (block.py):
+    rms_norm, rms_norm_backward     norm fused with residual sum and output gate
 """
 from __future__ import annotations
 
@@ -21,7 +22,7 @@ import os
 
 import torch
 
-__all__ = ["conv1d", "prefill", "decode_step", "gdn_layer", "prefill_workspace_size", "lib",
+__all__ = ["rms_norm", "rms_norm_backward", "conv1d", "prefill", "decode_step", "gdn_layer", "prefill_workspace_size", "lib",
            "prefill_backward", "conv1d_backward", "gdn_layer_backward", "GdnError", "LIB_PATH",
            "probe_mfma", "probe_copy", "prefill_noalloc", "NOALLOC_MAX_SEQS"]
 
@@ -121,6 +122,8 @@ def lib():
             f = getattr(L, name)
             f.argtypes = [ctypes.POINTER(argt)]
             f.restype = ctypes.c_size_t
+        from . import block
+        block.declare(L)
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_last_error.argtypes = []
@@ -525,3 +528,6 @@ def probe_copy(nbytes=1 << 30, reps=5, device=None):
         best = max(best, 2 * nbytes / (a.elapsed_time(b) * 1e-3) / 1e9)
     del src, dst
     return best
+
+
+from .block import rms_norm, rms_norm_backward  # noqa: E402

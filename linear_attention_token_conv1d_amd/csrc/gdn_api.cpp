@@ -9,54 +9,19 @@
 
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
 #include <cstddef>
-#include <cstdio>
-#include <cstdlib>
-#include <string>
 
+#include "api_util.h"
 #include "gdn_internal.h"
+
+namespace gdn {
+thread_local std::string g_last_error;
+}
 
 namespace {
 
-thread_local std::string g_last_error;
-
-gdn_status fail(gdn_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return s;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool debug_sync() {
-  static const bool on = [] {
-    const char* e = std::getenv("GDN_DEBUG");
-    return e && e[0] && e[0] != '0';
-  }();
-  return on;
-}
-
-gdn_status finish(hipError_t e, hipStream_t stream, const char* what) {
-  if (e == hipSuccess && debug_sync()) e = hipStreamSynchronize(stream);
-  if (e != hipSuccess) return fail(GDN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  g_last_error.clear();
-  return GDN_OK;
-}
-
-bool is_dtype(int32_t d) { return d == GDN_F32 || d == GDN_BF16; }
-size_t esize(int32_t d) { return d == GDN_BF16 ? 2 : 4; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || !na || !nb) return false;
-  const char* x = static_cast<const char*>(a);
-  const char* y = static_cast<const char*>(b);
-  return x < y + nb && y < x + na;
-}
+using namespace gdn::api;
+using gdn::g_last_error;
 
 // Fields added after ABI 3 read as their defaults from a shorter struct.
 int32_t prefill_state_dtype(const gdn_prefill_args* a) {

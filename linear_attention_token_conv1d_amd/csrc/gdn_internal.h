@@ -147,4 +147,59 @@ struct ConvBwdParams {
 size_t conv1d_backward_workspace_bytes(int64_t total_tokens, int channels);
 hipError_t launch_conv1d_backward(const ConvBwdParams& p, int dtype, hipStream_t stream);
 
+struct NormParams {
+  const void* x;
+  const void* weight;  // [width] or null
+  const void* gate;
+  const void* residual;
+  void* y;
+  void* sum;  // the pre order's residual + scale x
+  int64_t x_stride;
+  int64_t gate_stride;
+  int64_t residual_stride;
+  int64_t y_stride;
+  int64_t sum_stride;
+  int64_t rows;  // tokens * heads, < 2^31
+  int32_t heads;
+  int32_t width;
+  int32_t order;  // 0: norm after the sum, 1: sum after the norm
+  int32_t act;    // gate: 1 SiLU, 2 sigmoid
+  int32_t weight_bf16;
+  float eps;
+  float scale;
+  float weight_offset;
+};
+hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t stream);
+
+struct NormBwdParams {
+  const void* x;
+  const void* weight;
+  const void* gate;
+  const void* dy;
+  const void* d_sum;
+  void* dx;
+  void* d_residual;
+  void* dgate;
+  float* dweight;
+  int64_t x_stride;
+  int64_t gate_stride;
+  int64_t dy_stride;
+  int64_t d_sum_stride;
+  int64_t dx_stride;
+  int64_t d_residual_stride;
+  int64_t dgate_stride;
+  int64_t rows;
+  int32_t heads;
+  int32_t width;
+  int32_t order;
+  int32_t act;
+  int32_t weight_bf16;
+  float eps;
+  float scale;
+  float weight_offset;
+  void* workspace;  // partial dweight rows
+};
+size_t norm_backward_workspace_bytes(int64_t rows, int width);
+hipError_t launch_norm_backward(const NormBwdParams& p, int dtype, hipStream_t stream);
+
 }  // namespace gdn

@@ -1,0 +1,376 @@
+// gdn_rms_norm and gdn_rms_norm_backward kernels: RMS norm of rows, fused with
+// the residual sum ahead of it (or the residual sum after it), the residual
+// scale and the output gate.
+//
+//   pre :  h = residual + s x,  y = h r (w + c) act(z)          (y and h out)
+//   post:  y = residual + s x r (w + c) act(z)
+//   r = (mean(h^2) + eps)^-1/2 over the row (of x in the post order)
+//
+// Both directions are bound by the bytes they move: a row is read once into
+// registers by a group of lanes, reduced once, and written once.  The group is
+// as small as the row allows (16 lanes for a head of 128 in bf16, a wave up to
+// 1,024 elements, a workgroup beyond), so that short rows keep every lane busy
+// and need no LDS.  Statistics, products and sums are fp32; the only rounding
+// to the io dtype is each output's.  y of the pre order is formed from the
+// unrounded h.
+//
+// Backward, with n = h r, u = dy' (w + c) act(z), dy' = s dy in the post order:
+//   dh = r (u - n mean(u n)) + d_sum,   dz = dy' n (w + c) act'(z),
+//   dw = sum over rows of dy' n act(z).
+// mean(u n) = r mean(u h): both row sums (h^2 and u h) are taken in one pass.
+// dw: a group adds its rows in registers, the groups of a workgroup join in
+// LDS, each workgroup leaves one partial row, and a second kernel adds the
+// partial rows in order: the result does not depend on timing.
+#include "gdn_device.h"
+#include "gdn_internal.h"
+
+#include <type_traits>
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+  T v[VEC];
+};
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_pack(const void* base, int64_t at) {
+  return *reinterpret_cast<const Pack<T, VEC>*>(reinterpret_cast<const T*>(base) + at);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_pack(void* base, int64_t at, const float (&f)[VEC]) {
+  Pack<T, VEC> p;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) p.v[e] = from_f32<T>(f[e]);
+  *reinterpret_cast<Pack<T, VEC>*>(reinterpret_cast<T*>(base) + at) = p;
+}
+
+// weights are in the io dtype or in fp32 (gdn_rms_norm_args.weight_dtype)
+template <int VEC>
+__device__ __forceinline__ void load_weight(const void* w, int bf16, int at, float offset, float (&f)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    f[e] = w ? offset + (bf16 ? to_f32(reinterpret_cast<const __bf16*>(w)[at + e])
+                              : reinterpret_cast<const float*>(w)[at + e])
+             : 1.0f;
+  }
+}
+
+// Sigmoid: the hardware exponential for bf16 rows; for fp32 rows expf, whose
+// error stays at an ulp for large arguments.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z);
+template <>
+__device__ __forceinline__ float sigmoid<__bf16>(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+template <>
+__device__ __forceinline__ float sigmoid<float>(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// Sums of N values over a group of G lanes; every lane receives them.
+template <int G, int N>
+__device__ __forceinline__ void group_sum(float (&a)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = G == 16 ? row16_sum(a[i]) : wave_sum(a[i]);
+  if constexpr (G == kThreads) {
+    __shared__ float s[N][kThreads / 64];
+    __syncthreads();  // the previous row's sums have been read
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i][threadIdx.x >> 6] = a[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
+  }
+}
+
+template <typename T, int VEC, int G, int NV>
+__global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
+  const int lane = threadIdx.x % G;
+  int64_t row = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G;
+  const bool live = row < p.rows;
+  if (!live) row = p.rows - 1;  // a surplus group follows along without storing
+  const uint32_t t = (uint32_t)row / (uint32_t)p.heads;
+  const int64_t col = (int64_t)((uint32_t)row - t * (uint32_t)p.heads) * p.width;
+  const bool sum = p.order == 0 && p.residual;
+
+  Pack<T, VEC> x[NV], res[NV], z[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int at = (v * G + lane) * VEC;
+    if (at >= p.width) continue;
+    x[v] = load_pack<T, VEC>(p.x, t * p.x_stride + col + at);
+    if (p.residual) res[v] = load_pack<T, VEC>(p.residual, t * p.residual_stride + col + at);
+    if (p.gate) z[v] = load_pack<T, VEC>(p.gate, t * p.gate_stride + col + at);
+  }
+  float h[NV][VEC], ss[1] = {0.f};
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if ((v * G + lane) * VEC >= p.width) continue;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      h[v][e] = to_f32(x[v].v[e]);
+      if (sum) h[v][e] = fmaf(p.scale, h[v][e], to_f32(res[v].v[e]));
+      ss[0] = fmaf(h[v][e], h[v][e], ss[0]);
+    }
+  }
+  group_sum<G>(ss);
+  const float r = 1.0f / sqrtf(ss[0] / (float)p.width + p.eps);
+  if (!live) return;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int at = (v * G + lane) * VEC;
+    if (at >= p.width) continue;
+    float w[VEC], y[VEC];
+    load_weight<VEC>(p.weight, p.weight_bf16, at, p.weight_offset, w);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      y[e] = h[v][e] * r * w[e];
+      if (p.gate) {
+        const float zz = to_f32(z[v].v[e]), s = sigmoid<T>(zz);
+        y[e] *= p.act == 1 ? zz * s : s;
+      }
+      if (p.order == 1) y[e] = p.residual ? fmaf(p.scale, y[e], to_f32(res[v].v[e])) : p.scale * y[e];
+    }
+    if (sum) store_pack<T, VEC>(p.sum, t * p.sum_stride + col + at, h[v]);
+    store_pack<T, VEC>(p.y, t * p.y_stride + col + at, y);
+  }
+}
+
+template <typename T, int VEC, int G, int NV>
+__global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p, float* partial) {
+  constexpr int kGroups = kThreads / G;
+  const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  float dw[NV][VEC];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) dw[v][e] = 0.f;
+
+  // every group of a workgroup makes the same number of turns
+  for (int64_t first = (int64_t)blockIdx.x * kGroups; first < p.rows; first += (int64_t)gridDim.x * kGroups) {
+    const bool live = first + group < p.rows;
+    const uint32_t row = (uint32_t)(live ? first + group : p.rows - 1);
+    const uint32_t t = row / (uint32_t)p.heads;
+    const int64_t col = (int64_t)(row - t * (uint32_t)p.heads) * p.width;
+    Pack<T, VEC> x[NV], g[NV], z[NV], ds[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (v * G + lane) * VEC;
+      if (at >= p.width) continue;
+      x[v] = load_pack<T, VEC>(p.x, t * p.x_stride + col + at);
+      g[v] = load_pack<T, VEC>(p.dy, t * p.dy_stride + col + at);
+      if (p.gate) z[v] = load_pack<T, VEC>(p.gate, t * p.gate_stride + col + at);
+      if (p.d_sum) ds[v] = load_pack<T, VEC>(p.d_sum, t * p.d_sum_stride + col + at);
+    }
+    float sums[2] = {0.f, 0.f};  // of h^2 and of u h
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (v * G + lane) * VEC;
+      if (at >= p.width) continue;
+      float w[VEC];
+      load_weight<VEC>(p.weight, p.weight_bf16, at, p.weight_offset, w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float h = to_f32(x[v].v[e]);
+        float u = to_f32(g[v].v[e]) * w[e];
+        if (p.gate) {
+          const float zz = to_f32(z[v].v[e]), s = sigmoid<T>(zz);
+          u *= p.act == 1 ? zz * s : s;
+        }
+        sums[0] = fmaf(h, h, sums[0]);
+        sums[1] = fmaf(u, h, sums[1]);
+      }
+    }
+    group_sum<G>(sums);
+    const float r = 1.0f / sqrtf(sums[0] / (float)p.width + p.eps);
+    const float post = p.order == 1 ? p.scale : 1.0f;
+    const float c = r * r * sums[1] / (float)p.width;  // r mean(u n) = r^2 mean(u h)
+    if (live) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int at = (v * G + lane) * VEC;
+        if (at >= p.width) continue;
+        float w[VEC], dx[VEC], dz[VEC];
+        load_weight<VEC>(p.weight, p.weight_bf16, at, p.weight_offset, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float n = to_f32(x[v].v[e]) * r, dy = post * to_f32(g[v].v[e]);
+          float a = 1.f, slope = 0.f;
+          if (p.gate) {
+            const float zz = to_f32(z[v].v[e]), s = sigmoid<T>(zz);
+            a = p.act == 1 ? zz * s : s;
+            slope = p.act == 1 ? s * (1.f + zz * (1.f - s)) : s * (1.f - s);
+          }
+          dx[e] = r * (dy * w[e] * a) - n * (post * c);
+          if (p.d_sum) dx[e] += to_f32(ds[v].v[e]);
+          dz[e] = dy * n * w[e] * slope;
+          dw[v][e] = fmaf(dy * n, a, dw[v][e]);
+        }
+        if (p.d_residual) store_pack<T, VEC>(p.d_residual, t * p.d_residual_stride + col + at, dx);
+        if (p.dx) {
+          if (p.order == 0)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) dx[e] *= p.scale;
+          store_pack<T, VEC>(p.dx, t * p.dx_stride + col + at, dx);
+        }
+        if (p.gate) store_pack<T, VEC>(p.dgate, t * p.dgate_stride + col + at, dz);
+      }
+    }
+  }
+  if (!partial) return;
+  if constexpr (kGroups == 1) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (v * G + lane) * VEC;
+      if (at >= p.width) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) partial[(int64_t)blockIdx.x * p.width + at + e] = dw[v][e];
+    }
+  } else {
+    __shared__ float s[kGroups][G * NV * VEC];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s[group][(v * G + lane) * VEC + e] = dw[v][e];
+    __syncthreads();
+    for (int at = threadIdx.x; at < p.width; at += kThreads) {
+      float a = 0.f;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) a += s[k][at];
+      partial[(int64_t)blockIdx.x * p.width + at] = a;
+    }
+  }
+}
+
+// dw[c] = sum of the partial rows: 32 columns a workgroup, 32 row lanes whose
+// sums join in LDS in a fixed order.
+__global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* partial, int blocks, int width, float* dw) {
+  __shared__ float s[32][33];
+  const int c = threadIdx.x & 31, k = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+  float a = 0.f;
+  if (col < width)
+    for (int b = k; b < blocks; b += 32) a += partial[(int64_t)b * width + col];
+  s[k][c] = a;
+  __syncthreads();
+  if (k == 0 && col < width) {
+    float t = 0.f;
+    for (int i = 0; i < 32; ++i) t += s[i][c];
+    dw[col] = t;
+  }
+}
+
+bool vec_ok(const void* p, int64_t stride, int vec, size_t es) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (vec * es) == 0 && stride % vec == 0);
+}
+
+// Calls f with the template arguments that fit a row: VEC elements a load,
+// groups of G lanes, NV loads a lane.  `vec`: whether 16-byte loads are aligned.
+template <typename T, typename F>
+hipError_t dispatch(int width, bool vec, F&& f) {
+  constexpr int V = 16 / (int)sizeof(T);
+  auto with = [&](auto ve, auto g, auto nv) { return f.template operator()<decltype(ve)::value, decltype(g)::value, decltype(nv)::value>(); };
+#define GDN_NORM(VE, G, NV) \
+  return with(std::integral_constant<int, VE>{}, std::integral_constant<int, G>{}, std::integral_constant<int, NV>{})
+  if (vec && width % V == 0) {
+    const int n = width / V;
+    if (n <= 16) GDN_NORM(V, 16, 1);
+    if (n <= 64) GDN_NORM(V, 64, 1);
+    if (n <= 128) GDN_NORM(V, 64, 2);
+    const int per = (n + 255) / 256;
+    if (per <= 1) GDN_NORM(V, 256, 1);
+    if (per <= 2) GDN_NORM(V, 256, 2);
+    if (per <= 3) GDN_NORM(V, 256, 3);
+    if (per <= 4) GDN_NORM(V, 256, 4);
+    if (per <= 6) GDN_NORM(V, 256, 6);
+    if (per <= 8) GDN_NORM(V, 256, 8);
+    if constexpr (V == 4) GDN_NORM(V, 256, 16);
+  }
+  if (width <= 16) GDN_NORM(1, 16, 1);
+  if (width <= 128) GDN_NORM(1, 64, 2);
+  if (width <= 512) GDN_NORM(1, 64, 8);
+  if (width <= 2048) GDN_NORM(1, 256, 8);
+  if (width <= 6144) GDN_NORM(1, 256, 24);
+  GDN_NORM(1, 256, 64);
+#undef GDN_NORM
+}
+
+// The most workgroups of the backward: enough to fill the chip, few enough
+// that their partial dw rows stay small beside the rows themselves.
+int backward_blocks(int64_t rows, int width) {
+  const int64_t most = width <= 1024 ? 2048 : 1024;
+  return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
+}
+
+template <typename T>
+struct Forward {
+  const NormParams& p;
+  hipStream_t stream;
+  template <int VEC, int G, int NV>
+  hipError_t operator()() const {
+    const int64_t per = kThreads / G;
+    hipLaunchKernelGGL((norm_kernel<T, VEC, G, NV>), dim3((unsigned)((p.rows + per - 1) / per)), dim3(kThreads), 0,
+                       stream, p);
+    return hipGetLastError();
+  }
+};
+template <typename T>
+struct Backward {
+  const NormBwdParams& p;
+  hipStream_t stream;
+  int* blocks;  // in: the most; out: the number launched
+  template <int VEC, int G, int NV>
+  hipError_t operator()() const {
+    const int64_t need = (p.rows + kThreads / G - 1) / (kThreads / G);
+    if (need < *blocks) *blocks = (int)need;
+    hipLaunchKernelGGL((norm_backward_kernel<T, VEC, G, NV>), dim3((unsigned)*blocks), dim3(kThreads), 0, stream, p,
+                       p.dweight ? reinterpret_cast<float*>(p.workspace) : nullptr);
+    return hipGetLastError();
+  }
+};
+
+template <typename T>
+hipError_t forward(const NormParams& p, hipStream_t stream) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const size_t es = sizeof(T);
+  const bool vec = p.width % V == 0 && vec_ok(p.x, p.x_stride, V, es) && vec_ok(p.gate, p.gate_stride, V, es) &&
+                   vec_ok(p.residual, p.residual_stride, V, es) && vec_ok(p.y, p.y_stride, V, es) &&
+                   vec_ok(p.sum, p.sum_stride, V, es);
+  return dispatch<T>(p.width, vec, Forward<T>{p, stream});
+}
+template <typename T>
+hipError_t backward(const NormBwdParams& p, hipStream_t stream, int* blocks) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const size_t es = sizeof(T);
+  const bool vec = p.width % V == 0 && vec_ok(p.x, p.x_stride, V, es) && vec_ok(p.gate, p.gate_stride, V, es) &&
+                   vec_ok(p.dy, p.dy_stride, V, es) && vec_ok(p.d_sum, p.d_sum_stride, V, es) &&
+                   vec_ok(p.dx, p.dx_stride, V, es) && vec_ok(p.dgate, p.dgate_stride, V, es) &&
+                   vec_ok(p.d_residual, p.d_residual_stride, V, es);
+  return dispatch<T>(p.width, vec, Backward<T>{p, stream, blocks});
+}
+
+}  // namespace
+
+size_t norm_backward_workspace_bytes(int64_t rows, int width) {
+  return (size_t)backward_blocks(rows, width) * width * sizeof(float);
+}
+
+hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t stream) {
+  if (p.rows == 0) return hipSuccess;
+  return dtype == 1 ? forward<__bf16>(p, stream) : forward<float>(p, stream);
+}
+
+hipError_t launch_norm_backward(const NormBwdParams& p, int dtype, hipStream_t stream) {
+  int blocks = 0;  // no rows: dw is the sum of nothing
+  if (p.rows > 0) {
+    blocks = backward_blocks(p.rows, p.width);
+    const hipError_t e = dtype == 1 ? backward<__bf16>(p, stream, &blocks) : backward<float>(p, stream, &blocks);
+    if (e != hipSuccess) return e;
+  }
+  if (!p.dweight) return hipSuccess;
+  hipLaunchKernelGGL(norm_dweight_kernel, dim3((unsigned)((p.width + 31) / 32)), dim3(1024), 0, stream,
+                     reinterpret_cast<const float*>(p.workspace), blocks, p.width, p.dweight);
+  return hipGetLastError();
+}
+
+}  // namespace gdn
