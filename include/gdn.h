@@ -565,6 +565,188 @@ size_t gdn_rms_norm_backward_workspace_size(const gdn_rms_norm_backward_args* ar
 
 gdn_status gdn_rms_norm_backward(const gdn_rms_norm_backward_args* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * gdn_rope -- rotary positions on the query and key heads of an attention
+ * layer, and (inverse) the gradient of that rotation.
+ *
+ *   angle[t, i] = positions[t] * inv_freq[i],  i < rot / 2
+ *   (a, b) -> mscale (a cos - b sin, b cos + a sin)
+ *   for the pairs (i, i + rot/2) of a head (GDN_ROPE_HALF) or (2i, 2i + 1)
+ *   (GDN_ROPE_INTERLEAVED); elements rot .. d - 1 of a head pass through.
+ *   Angles are reduced in fp64, so far positions lose nothing; products are
+ *   fp32, each output is rounded once.
+ *
+ *   dtype        GDN_BF16 or GDN_F32: dtype of q, k and their outputs.
+ *   layout       GDN_ROPE_HALF or GDN_ROPE_INTERLEAVED.
+ *   inverse      1 rotates by the opposite angle: given the gradients of the
+ *                outputs this writes those of the inputs.
+ *   positions    [tokens] int32 or int64 (position_bits = 32 or 64).
+ *   inv_freq     [rot / 2] fp64 radians a position: scaled as a long-context
+ *                scheme asks, if any; mscale is such a scheme's factor on the
+ *                cosines and sines (1 otherwise).
+ *   h_q, h_k     heads; h_k = 0 without k.   d >= 2, rot even, 2..d.
+ *   q, q_out     [tokens, h_q, d], k, k_out [tokens, h_k, d] with token
+ *                strides in elements (heads contiguous inside a token).  16-byte
+ *                accesses are used where pointers, strides, d and rot allow
+ *                them; any element-aligned layout is valid.  An output may be
+ *                its input itself (same pointer and stride).
+ * ---------------------------------------------------------------------- */
+typedef enum gdn_rope_layout { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+
+typedef struct gdn_rope_args {
+  uint32_t struct_size;
+  int32_t dtype;
+  int32_t layout;
+  int32_t inverse;
+  int32_t position_bits;
+  int32_t h_q;
+  int32_t h_k;
+  int32_t d;
+  int32_t rot;
+  float mscale;
+  int64_t tokens;
+  const void* q;
+  const void* k;
+  const void* positions;
+  const double* inv_freq;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t q_out_stride;
+  int64_t k_out_stride;
+} gdn_rope_args;
+
+gdn_status gdn_rope(const gdn_rope_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * gdn_cache_store -- new keys and values into a paged 8-bit cache, with one
+ * scale for each page and head.
+ *
+ * A page holds page_size tokens of one sequence: codes in OCP e4m3 (value =
+ * code * scale), keys as [page_size][d], values as [d][page_size], the order
+ * in which attention reads them.  Token position i of sequence n lies in slot
+ * i % page_size of page page_table[n, i / page_size].
+ *   scale = the least power of two that takes the largest finite magnitude of
+ *           the page's tokens in this call to at most 448, and at least the
+ *           page's present scale where the page holds older tokens of the
+ *           sequence; those are rounded anew where it grows (an exact
+ *           division, but for what falls among e4m3's subnormals).
+ * Values are rounded to nearest even; infinities saturate, NaN stays NaN.
+ *
+ *   io_dtype     GDN_BF16 or GDN_F32: dtype of k and v.
+ *   n_seqs       >= 1;  h_kv >= 1 (<= 65535);  d 64, 128 or 256;
+ *   page_size    16, 32, 64, 128 or 256;  pages >= 1: pages of the pool;
+ *   max_pages    >= 1: columns of page_table.
+ *   k, v         [tokens, h_kv, d] with token strides (16-byte aligned, strides
+ *                multiples of 8 elements, heads contiguous inside a token).
+ *   k_cache      [pages, h_kv, page_size, d], v_cache [pages, h_kv, d, page_size]
+ *                e4m3, 16-byte aligned;  k_scale, v_scale [pages, h_kv] fp32.
+ *   page_table   [n_seqs, max_pages] int32.
+ *   lens         [n_seqs] int32: tokens each sequence held before the call.
+ *   cu_seqlens   [n_seqs + 1] int32 offsets of each sequence's new tokens, or
+ *                NULL: tokens / n_seqs new tokens for each (a whole number).
+ *                Tokens from cu_seqlens[n_seqs] on (a padded batch) are left
+ *                alone.
+ * Tables and lengths are not read on the host.  A token whose page lies
+ * outside the pool or behind the table's last column is not stored.  A page
+ * that a call writes to belongs to one sequence of it.
+ * ---------------------------------------------------------------------- */
+typedef struct gdn_cache_store_args {
+  uint32_t struct_size;
+  int32_t io_dtype;
+  int32_t n_seqs;
+  int32_t h_kv;
+  int32_t d;
+  int32_t page_size;
+  int32_t pages;
+  int32_t max_pages;
+  int64_t tokens;
+  const void* k;
+  const void* v;
+  int64_t k_stride;
+  int64_t v_stride;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  const int32_t* lens;
+  const int32_t* cu_seqlens;
+} gdn_cache_store_args;
+
+gdn_status gdn_cache_store(const gdn_cache_store_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * gdn_cache_attention -- softmax attention of each sequence's newest tokens
+ * over its pages of an 8-bit cache (gdn_cache_store), the new tokens' own keys
+ * and values among them: the hybrid's other token mixer, for single tokens,
+ * several tokens a sequence and whole chunks of prompts.
+ *
+ *   o[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j  (* sigmoid(gate[t, h]))
+ *   over the keys j of head h / (h_q / h_kv) that the token sees.  Token i of a
+ *   sequence's L new ones has position lens[n] - L + i; it sees positions up
+ *   to its own (causal) or below lens[n] (not causal), and with a window only
+ *   those above its own minus window.  A token that sees nothing gives zeros.
+ *
+ *   io_dtype     GDN_BF16 or GDN_F32: dtype of q, gate and o.  Softmax, sums
+ *                and accumulators are fp32 whichever it is.
+ *   h_q, h_kv    h_q % h_kv == 0, h_kv <= 65535;  d 64, 128 or 256.
+ *   causal       0 or 1;  window >= 0 (0: none);  scale > 0, finite.
+ *   q, gate, o   [tokens, h_q, d] with token strides (16-byte aligned, strides
+ *                multiples of 8 elements, heads contiguous inside a token);
+ *                gate may be NULL.  o may be q itself.
+ *   lse          [tokens, h_q] fp32: log of the sum of exponentials (natural;
+ *                -inf where nothing is seen), or NULL.
+ *   lens         [n_seqs] int32: tokens in the cache, the new ones among them.
+ *   cu_seqlens   as in gdn_cache_store; rows of a padded batch behind the last
+ *                sequence are not written.
+ *   workspace    gdn_cache_attention_workspace_size() bytes, 256-byte aligned:
+ *                partial results of long contexts cut into pieces.
+ *   The cache and its table as in gdn_cache_store (scales of any positive
+ *   value, e4m3 codes written by others too); a page outside the pool holds no
+ *   tokens.  tokens * h_q / h_kv < 2^31.
+ * NaN and infinities in keys or values that a token does not see do not
+ * reach it.
+ * ---------------------------------------------------------------------- */
+typedef struct gdn_cache_attention_args {
+  uint32_t struct_size;
+  int32_t io_dtype;
+  int32_t n_seqs;
+  int32_t h_q;
+  int32_t h_kv;
+  int32_t d;
+  int32_t page_size;
+  int32_t pages;
+  int32_t max_pages;
+  int32_t causal;
+  int32_t window;
+  float scale;
+  int64_t tokens;
+  const void* q;
+  const void* gate;
+  void* o;
+  int64_t q_stride;
+  int64_t gate_stride;
+  int64_t o_stride;
+  float* lse;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* page_table;
+  const int32_t* lens;
+  const int32_t* cu_seqlens;
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_cache_attention_args;
+
+/* Pointers are not read, but whether cu_seqlens is NULL; 0 also when the
+ * arguments are invalid. */
+size_t gdn_cache_attention_workspace_size(const gdn_cache_attention_args* args);
+
+gdn_status gdn_cache_attention(const gdn_cache_attention_args* args, void* stream);
+
 /* Diagnostics. */
 const char* gdn_status_string(gdn_status status);
 const char* gdn_last_error(void); /* thread-local detail of the last failure */

@@ -14,6 +14,9 @@ Entry points (same names as the C ABI):
 and gdn_layer / gdn_layer_backward, which chain them for a whole token mixer
 layer.  Around the mixer in a hybrid block (block.py):
     rms_norm, rms_norm_backward     norm fused with residual sum and output gate
+    rope, rope_backward             rotary positions (rope_frequencies makes their table)
+    cache_store                     new keys and values into a paged 8-bit cache (kv_cache)
+    cache_attention                 attention of the newest tokens over that cache
 """
 from __future__ import annotations
 
@@ -22,7 +25,8 @@ import os
 
 import torch
 
-__all__ = ["rms_norm", "rms_norm_backward", "conv1d", "prefill", "decode_step", "gdn_layer", "prefill_workspace_size", "lib",
+__all__ = ["rms_norm", "rms_norm_backward", "rope", "rope_backward", "rope_frequencies", "KVCache", "kv_cache", "cache_store",
+           "cache_attention", "cache_attention_workspace_size", "conv1d", "prefill", "decode_step", "gdn_layer", "prefill_workspace_size", "lib",
            "prefill_backward", "conv1d_backward", "gdn_layer_backward", "GdnError", "LIB_PATH",
            "probe_mfma", "probe_copy", "prefill_noalloc", "NOALLOC_MAX_SEQS"]
 
@@ -530,4 +534,5 @@ def probe_copy(nbytes=1 << 30, reps=5, device=None):
     return best
 
 
-from .block import rms_norm, rms_norm_backward  # noqa: E402
+from .block import (KVCache, cache_attention, cache_attention_workspace_size, cache_store, kv_cache,  # noqa: E402
+                    rms_norm, rms_norm_backward, rope, rope_backward, rope_frequencies)

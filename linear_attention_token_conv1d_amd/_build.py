@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
 SOURCES = ["gdn_api.cpp", "conv1d.hip", "decode.hip", "prefill.hip", "backward.hip", "probe.hip",
-           "block_api.cpp", "norm.hip"]
+           "block_api.cpp", "norm.hip", "rope.hip", "kv_cache.hip", "attention.hip"]
 
 FLAGS = [
     f"--offload-arch={ARCH}",

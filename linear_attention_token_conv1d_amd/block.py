@@ -8,7 +8,9 @@ which need not be the current device.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
+import math
 
 import torch
 
@@ -40,13 +42,41 @@ class NormBwdArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", _i32), ("layout", _i32), ("inverse", _i32),
+                ("position_bits", _i32), ("h_q", _i32), ("h_k", _i32), ("d", _i32), ("rot", _i32), ("mscale", _f32),
+                ("tokens", _i64), ("q", _c_void_p), ("k", _c_void_p), ("positions", _c_void_p), ("inv_freq", _c_void_p),
+                ("q_out", _c_void_p), ("k_out", _c_void_p), ("q_stride", _i64), ("k_stride", _i64),
+                ("q_out_stride", _i64), ("k_out_stride", _i64)]
+
+
+class CacheStoreArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("io_dtype", _i32), ("n_seqs", _i32), ("h_kv", _i32), ("d", _i32),
+                ("page_size", _i32), ("pages", _i32), ("max_pages", _i32), ("tokens", _i64), ("k", _c_void_p),
+                ("v", _c_void_p), ("k_stride", _i64), ("v_stride", _i64), ("k_cache", _c_void_p), ("v_cache", _c_void_p),
+                ("k_scale", _c_void_p), ("v_scale", _c_void_p), ("page_table", _c_void_p), ("lens", _c_void_p),
+                ("cu_seqlens", _c_void_p)]
+
+
+class CacheAttentionArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("io_dtype", _i32), ("n_seqs", _i32), ("h_q", _i32), ("h_kv", _i32),
+                ("d", _i32), ("page_size", _i32), ("pages", _i32), ("max_pages", _i32), ("causal", _i32),
+                ("window", _i32), ("scale", _f32), ("tokens", _i64), ("q", _c_void_p), ("gate", _c_void_p),
+                ("o", _c_void_p), ("q_stride", _i64), ("gate_stride", _i64), ("o_stride", _i64), ("lse", _c_void_p),
+                ("k_cache", _c_void_p), ("v_cache", _c_void_p), ("k_scale", _c_void_p), ("v_scale", _c_void_p),
+                ("page_table", _c_void_p), ("lens", _c_void_p), ("cu_seqlens", _c_void_p), ("workspace", _c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 def declare(L):
     """Argument types of this module's entry points in the loaded library."""
-    for name, argt in (("gdn_rms_norm", NormArgs), ("gdn_rms_norm_backward", NormBwdArgs)):
+    for name, argt in (("gdn_rms_norm", NormArgs), ("gdn_rms_norm_backward", NormBwdArgs), ("gdn_rope", RopeArgs),
+                       ("gdn_cache_store", CacheStoreArgs), ("gdn_cache_attention", CacheAttentionArgs)):
         f = getattr(L, name)
         f.argtypes = [ctypes.POINTER(argt), _c_void_p]
         f.restype = ctypes.c_int
-    for name, argt in (("gdn_rms_norm_backward_workspace_size", NormBwdArgs),):
+    for name, argt in (("gdn_rms_norm_backward_workspace_size", NormBwdArgs),
+                       ("gdn_cache_attention_workspace_size", CacheAttentionArgs)):
         f = getattr(L, name)
         f.argtypes = [ctypes.POINTER(argt)]
         f.restype = ctypes.c_size_t
@@ -206,3 +236,206 @@ def _workspace(given, need, index, dev):
         if given.numel() >= need and given.is_contiguous():
             return given
     return torch.empty(need, dtype=torch.uint8, device=dev)
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=None, low=1.0, high=32.0, device=None):
+    """Radians a position for each of the rot / 2 pairs of a rotated head, fp64
+    [rot / 2], and the factor on the cosines and sines (rope's inv_freq and
+    mscale).
+
+    scaling=None: base^(-2 i / rot).  For contexts `factor` times longer:
+    "linear" divides every frequency by factor; "ntk" raises the base so that
+    the slowest pair is divided by it and the fastest keeps its frequency;
+    "by_parts" keeps pairs that turn more than `high` times over the original
+    context, divides those that turn less than `low` times, blends between,
+    and returns the factor 0.1 ln(factor) + 1."""
+    if rot < 2 or rot % 2:
+        raise GdnError(f"rot must be even and positive, got {rot}")
+    if not factor >= 1.0:
+        raise GdnError(f"factor must be at least 1, got {factor}")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        base = base * factor ** (rot / (rot - 2)) if rot > 2 else base
+    f = float(base) ** (-2 * i / rot)
+    m = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        if not original or not 0 < low < high:
+            raise GdnError("by_parts needs the original context length and 0 < low < high")
+        turns = original * f / (2 * math.pi)
+        kept = ((turns - low) / (high - low)).clamp(0, 1)
+        f = f * kept + f / factor * (1 - kept)
+        m = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise GdnError(f"scaling must be None, 'linear', 'ntk' or 'by_parts', got {scaling!r}")
+    return f.to(device) if device is not None else f, m
+
+
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+
+
+def _heads(t, name, index, dtype):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise GdnError(f"{name} must be a [T, H, d] tensor")
+    return _rows(t, name, index, t.shape, dtype)
+
+
+def _rope(q, positions, inv_freq, k, layout, mscale, inverse, out, k_out):
+    index = _gpu(q, "q")
+    if q.dtype not in _DT:
+        raise GdnError(f"q must be torch.bfloat16 or torch.float32, got {q.dtype}")
+    if layout not in ROPE_LAYOUT:
+        raise GdnError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+    dt = q.dtype
+    pq, sq = _heads(q, "q", index, dt)
+    T, h_q, d = q.shape
+    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int64, torch.int32):
+        raise GdnError("positions must be a torch.int32 or torch.int64 tensor")
+    pp = _tensor(positions, "positions", index, (T,), positions.dtype)
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise GdnError("inv_freq must be a [rot / 2] tensor")
+    pf = _tensor(inv_freq, "inv_freq", index, inv_freq.shape, torch.float64)
+    y = torch.empty(q.shape, dtype=dt, device=q.device) if out is None else out
+    py, sy = _rows(y, "out", index, q.shape, dt)
+    h_k, pk, sk, pz, sz, z = 0, None, 0, None, 0, None
+    if k is not None:
+        pk, sk = _heads(k, "k", index, dt)
+        if k.shape[0] != T or k.shape[2] != d:
+            raise GdnError(f"k must be [{T}, H, {d}], got {list(k.shape)}")
+        h_k = k.shape[1]
+        z = torch.empty(k.shape, dtype=dt, device=q.device) if k_out is None else k_out
+        pz, sz = _rows(z, "k_out", index, k.shape, dt)
+    elif k_out is not None:
+        raise GdnError("k_out goes with k")
+    a = RopeArgs(ctypes.sizeof(RopeArgs), _DT[dt], ROPE_LAYOUT[layout], inverse, 64 if positions.dtype == torch.int64 else 32,
+                 h_q, h_k, d, 2 * inv_freq.shape[0], mscale, T, pq, pk, pp, pf, py, pz, sq, sk, sy, sz)
+    _run("gdn_rope", a, index)
+    return y if k is None else (y, z)
+
+
+def rope(q, positions, inv_freq, k=None, layout="half", mscale=1.0, out=None, k_out=None):
+    """Rotary positions on the heads of q [T, H, d], and of k [T, H_k, d] in the
+    same launch (bf16 or fp32, token stride free): returns q' or (q', k').
+
+    positions [T] (int32 or int64) are the tokens' positions, inv_freq
+    [rot / 2] fp64 the radians a position of each pair (rope_frequencies);
+    rot may be less than d: the rest of a head passes through.  layout "half"
+    pairs elements i and i + rot / 2, "interleaved" 2 i and 2 i + 1.  out and
+    k_out may be q and k themselves (in place)."""
+    return _rope(q, positions, inv_freq, k, layout, mscale, 0, out, k_out)
+
+
+def rope_backward(dq, positions, inv_freq, k=None, layout="half", mscale=1.0, out=None, k_out=None):
+    """Gradients of rope's inputs given those of its outputs (dq, and k: that of
+    k'): the rotation by the opposite angle.  Arguments as in rope."""
+    return _rope(dq, positions, inv_freq, k, layout, mscale, 1, out, k_out)
+
+
+FP8 = torch.float8_e4m3fn
+KVCache = collections.namedtuple("KVCache", "k v k_scale v_scale")
+
+
+def kv_cache(pages, h_kv, d, page_size=64, device="cuda"):
+    """An empty pool of pages: e4m3 keys [pages, h_kv, page_size, d] and values
+    [pages, h_kv, d, page_size], and their fp32 scales [pages, h_kv]."""
+    def new(*shape, dtype):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+    return KVCache(new(pages, h_kv, page_size, d, dtype=torch.uint8).view(FP8), new(pages, h_kv, d, page_size, dtype=torch.uint8).view(FP8),
+                   new(pages, h_kv, dtype=torch.float32), new(pages, h_kv, dtype=torch.float32))
+
+
+def _cache(cache, index, h_kv, d):
+    if len(cache) != 4 or not isinstance(cache[0], torch.Tensor) or cache[0].dim() != 4:
+        raise GdnError("cache must be (k [pages, h_kv, page_size, d], v, k_scale, v_scale)")
+    k, v, ks, vs = cache
+    pages, h, page = k.shape[:3]
+    if h != h_kv or k.shape[3] != d:
+        raise GdnError(f"the cache holds {h} heads of {k.shape[3]}, not {h_kv} of {d}")
+    return (pages, page, _tensor(k, "cache.k", index, k.shape, FP8), _tensor(v, "cache.v", index, (pages, h, d, page), FP8),
+            _tensor(ks, "cache.k_scale", index, (pages, h), torch.float32), _tensor(vs, "cache.v_scale", index, (pages, h), torch.float32))
+
+
+def _sequences(page_table, lens, cu_seqlens, index, tokens):
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise GdnError("page_table must be [n_seqs, max_pages]")
+    n, width = page_table.shape
+    pt = _tensor(page_table, "page_table", index, page_table.shape, torch.int32)
+    pl = _tensor(lens, "lens", index, (n,), torch.int32)
+    if pl is None:
+        raise GdnError("lens is required")
+    pc = _tensor(cu_seqlens, "cu_seqlens", index, (n + 1,), torch.int32)
+    if pc is None and n and tokens % n:
+        raise GdnError(f"without cu_seqlens every sequence has the same number of new tokens: {tokens} over {n} sequences")
+    return n, width, pt, pl, pc
+
+
+def cache_store(k, v, cache, page_table, lens, cu_seqlens=None):
+    """Store new keys and values [T, H_kv, d] (bf16 or fp32, token stride free)
+    in the pages of `cache` (kv_cache), in place.
+
+    page_table [N, M] int32 names the pages of each sequence, lens [N] int32
+    the tokens it held before.  cu_seqlens [N + 1] int32 are the offsets of
+    each sequence's new tokens; without it each has T / N.  Each page and head
+    gets the least power of two as its scale that holds its largest value; a
+    page that holds older tokens keeps a larger scale, or has them rounded
+    anew by the new one.  Tokens behind the table or on a page outside the
+    pool (say -1) are not stored."""
+    index = _gpu(k, "k")
+    if k.dtype not in _DT:
+        raise GdnError(f"k must be torch.bfloat16 or torch.float32, got {k.dtype}")
+    pk, sk = _heads(k, "k", index, k.dtype)
+    T, h, d = k.shape
+    pv, sv = _rows(v, "v", index, k.shape, k.dtype)
+    pages, page, pkc, pvc, pks, pvs = _cache(cache, index, h, d)
+    n, width, pt, pl, pc = _sequences(page_table, lens, cu_seqlens, index, T)
+    a = CacheStoreArgs(ctypes.sizeof(CacheStoreArgs), _DT[k.dtype], n, h, d, page, pages, width, T, pk, pv, sk, sv, pkc, pvc, pks, pvs,
+                       pt, pl, pc)
+    _run("gdn_cache_store", a, index)
+
+
+def cache_attention(q, cache, page_table, lens, cu_seqlens=None, scale=None, causal=True, window=0, gate=None, out=None,
+                    return_lse=False, workspace=None):
+    """Attention of each sequence's newest tokens q [T, H_q, d] over its pages of
+    `cache`, where their own keys and values lie already (cache_store).
+
+    lens [N] int32 counts the tokens in the cache, the new ones among them;
+    cu_seqlens [N + 1] int32 are the offsets of the new tokens (T / N each
+    without it).  scale is d^-1/2 by default.  causal: a token sees positions
+    up to its own; window > 0: only those above its own minus window.  gate
+    (like q) multiplies the output by its sigmoid.  Returns o like q, or
+    (o, lse [T, H_q] fp32) with return_lse; a token that sees nothing gives
+    zeros and -inf.  Rows behind the last sequence of a padded batch are not
+    written."""
+    index = _gpu(q, "q")
+    if q.dtype not in _DT:
+        raise GdnError(f"q must be torch.bfloat16 or torch.float32, got {q.dtype}")
+    dt = q.dtype
+    pq, sq = _heads(q, "q", index, dt)
+    T, h_q, d = q.shape
+    if not isinstance(cache[0], torch.Tensor) or cache[0].dim() != 4:
+        raise GdnError("cache must be (k [pages, h_kv, page_size, d], v, k_scale, v_scale)")
+    h = cache[0].shape[1]
+    pages, page, pkc, pvc, pks, pvs = _cache(cache, index, h, d)
+    n, width, pt, pl, pc = _sequences(page_table, lens, cu_seqlens, index, T)
+    pg, sg = _rows(gate, "gate", index, q.shape, dt)
+    o = torch.empty(q.shape, dtype=dt, device=q.device) if out is None else out
+    po, so = _rows(o, "out", index, q.shape, dt)
+    lse = torch.empty((T, h_q), dtype=torch.float32, device=q.device) if return_lse else None
+    a = CacheAttentionArgs(ctypes.sizeof(CacheAttentionArgs), _DT[dt], n, h_q, h, d, page, pages, width, 1 if causal else 0, window,
+                           d ** -0.5 if scale is None else scale, T, pq, pg, po, sq, sg, so, None if lse is None else lse.data_ptr(), pkc,
+                           pvc, pks, pvs, pt, pl, pc)
+    need = lib().gdn_cache_attention_workspace_size(a)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, index, q.device)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    _run("gdn_cache_attention", a, index)
+    return (o, lse) if return_lse else o
+
+
+def cache_attention_workspace_size(tokens, n_seqs, max_pages, h_q, h_kv, d, page_size=64, ragged=False):
+    """Bytes of workspace that cache_attention needs (0: none) for a caller that keeps one."""
+    a = CacheAttentionArgs(struct_size=ctypes.sizeof(CacheAttentionArgs), n_seqs=n_seqs, h_q=h_q, h_kv=h_kv, d=d, page_size=page_size,
+                           max_pages=max_pages, tokens=tokens, cu_seqlens=1 if ragged else None)
+    return lib().gdn_cache_attention_workspace_size(a)

@@ -202,4 +202,103 @@ struct NormBwdParams {
 size_t norm_backward_workspace_bytes(int64_t rows, int width);
 hipError_t launch_norm_backward(const NormBwdParams& p, int dtype, hipStream_t stream);
 
+struct RopeParams {
+  const void* q;
+  const void* k;  // null with h_k = 0
+  const void* positions;
+  const double* inv_freq;  // [rot / 2]
+  void* q_out;
+  void* k_out;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t q_out_stride;
+  int64_t k_out_stride;
+  int64_t tokens;
+  int32_t pos64;  // positions are int64 (else int32)
+  int32_t h_q;
+  int32_t h_k;
+  int32_t d;
+  int32_t rot;
+  int32_t half;
+  int32_t inverse;
+  float mscale;
+  // set by the launcher: units of a head, head groups of a token, heads of a group
+  int32_t units;
+  int32_t splits;
+  int32_t per;
+};
+hipError_t launch_rope(const RopeParams& p, int dtype, hipStream_t stream);
+
+struct CacheStoreParams {
+  const void* k;
+  const void* v;
+  uint8_t* k_cache;  // [pages, h_kv, page, d]
+  uint8_t* v_cache;  // [pages, h_kv, d, page]
+  float* k_scale;    // [pages, h_kv]
+  float* v_scale;
+  const int32_t* page_table;  // [n_seqs, max_pages]
+  const int32_t* lens;        // [n_seqs] tokens held before the call
+  const int32_t* cu_seqlens;  // or null: tokens / n_seqs new ones for each
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t tokens;
+  int32_t n_seqs;
+  int32_t h_kv;
+  int32_t d;
+  int32_t page;
+  int32_t pages;
+  int32_t max_pages;
+  // set by the launcher: new tokens of a sequence and workgroups for its pages
+  int64_t uniform;
+  int32_t uniform_slots;
+};
+hipError_t launch_cache_store(const CacheStoreParams& p, int dtype, hipStream_t stream);
+
+// What decides how a call of gdn_cache_attention is cut up.
+struct AttendShape {
+  int64_t tokens;
+  int32_t n_seqs;
+  int32_t h_q;
+  int32_t h_kv;
+  int32_t d;
+  int32_t page;
+  int32_t max_pages;
+  int32_t ragged;
+};
+struct AttendParams {
+  const void* q;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* page_table;
+  const int32_t* lens;  // [n_seqs] tokens in the cache, the new ones among them
+  const int32_t* cu_seqlens;
+  const void* gate;
+  void* o;
+  float* lse;
+  int64_t q_stride;
+  int64_t gate_stride;
+  int64_t o_stride;
+  int64_t tokens;
+  int32_t n_seqs;
+  int32_t h_q;
+  int32_t h_kv;
+  int32_t page_shift;
+  int32_t pages;
+  int32_t max_pages;
+  int32_t causal;
+  int32_t window;  // 0: none
+  float scale_log2;  // scale * log2(e)
+  // set by the launcher
+  int32_t max_tokens;
+  int32_t uniform_tiles;
+  int64_t uniform;
+  int32_t piece;
+  float* part_o;   // [pieces, tokens, h_q, d]
+  float* part_ml;  // [pieces, tokens, h_q, 2]
+};
+size_t attend_workspace_bytes(const AttendShape& a);
+hipError_t launch_attend(AttendParams p, const AttendShape& a, void* workspace, int dtype, hipStream_t stream);
+
 }  // namespace gdn

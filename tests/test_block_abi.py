@@ -11,7 +11,8 @@ import linear_attention_token_conv1d_amd as gdn
 from linear_attention_token_conv1d_amd import block
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-STRUCTS = {"gdn_rms_norm_args": block.NormArgs, "gdn_rms_norm_backward_args": block.NormBwdArgs}
+STRUCTS = {"gdn_rms_norm_args": block.NormArgs, "gdn_rms_norm_backward_args": block.NormBwdArgs, "gdn_rope_args": block.RopeArgs,
+           "gdn_cache_store_args": block.CacheStoreArgs, "gdn_cache_attention_args": block.CacheAttentionArgs}
 
 
 def test_structs_match_the_header():
@@ -90,3 +91,79 @@ def test_wrappers_need_gpu_tensors():
         gdn.rms_norm(x)
     with pytest.raises(gdn.GdnError, match="GPU"):
         gdn.rms_norm_backward(x, x)
+
+
+ROPE = dict(dtype=1, position_bits=64, h_q=2, h_k=1, d=64, rot=32, mscale=1.0, tokens=4, q=0x10000, k=0x20000, positions=0x30000,
+            inv_freq=0x40000, q_out=0x50000, k_out=0x60000, q_stride=128, k_stride=64, q_out_stride=128, k_out_stride=64)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(struct_size=8), 1), (dict(dtype=3), 1), (dict(layout=2), 1), (dict(inverse=2), 1), (dict(position_bits=16), 1), (dict(h_q=0), 1),
+    (dict(h_k=-1), 1), (dict(d=1), 1), (dict(rot=0), 1), (dict(rot=33), 1), (dict(rot=66), 1), (dict(mscale=float("nan")), 1),
+    (dict(tokens=-1), 1), (dict(q=0), 1), (dict(k=0), 1), (dict(k_out=0), 1), (dict(h_k=0), 1), (dict(positions=0x30004), 3),
+    (dict(inv_freq=0x40004), 3), (dict(q_stride=127), 1), (dict(q=0x10001), 3), (dict(q_out=0x10080), 1), (dict(q_out=0x20000), 1),
+    (dict(k_out=0x50000), 1), (dict(q_out=0x30000), 1), (dict(q_out=0x10000, q_out_stride=256), 1),
+])
+def test_rope_refusals(kw, code):
+    st, msg = _call("gdn_rope", block.RopeArgs, ROPE, kw)
+    assert st == code and msg.startswith("gdn_rope"), msg
+
+
+POOL = dict(io_dtype=1, n_seqs=2, h_kv=2, d=64, page_size=16, pages=8, max_pages=4, tokens=4, k_cache=0x1000000, v_cache=0x2000000,
+            k_scale=0x3000000, v_scale=0x4000000, page_table=0x50000, lens=0x60000)
+STORE = dict(POOL, k=0x10000, v=0x20000, k_stride=128, v_stride=128)
+ATTEND = dict(POOL, h_q=4, causal=1, scale=0.125, q=0x10000, o=0x20000, q_stride=256, gate_stride=256, o_stride=256)
+POOL_BAD = [
+    (dict(struct_size=8), 1), (dict(io_dtype=2), 1), (dict(n_seqs=0), 1), (dict(tokens=-2), 1), (dict(tokens=5), 1), (dict(h_kv=0), 1),
+    (dict(h_kv=65536), 1), (dict(d=96), 2), (dict(page_size=48), 2), (dict(page_size=8), 2), (dict(page_size=512), 2), (dict(pages=0), 1),
+    (dict(max_pages=0), 1), (dict(k_cache=0), 1), (dict(v_scale=0), 1), (dict(page_table=0), 1), (dict(lens=0), 1),
+    (dict(v_cache=0x2000008), 3), (dict(k_scale=0x3000002), 3), (dict(cu_seqlens=0x70001), 3), (dict(tokens=1 << 31), 1),
+]
+
+
+@pytest.mark.parametrize("kw,code", POOL_BAD + [
+    (dict(k=0), 1), (dict(k_stride=127), 1), (dict(v_stride=132), 3), (dict(v=0x20008), 3), (dict(v_cache=0x1000100), 1),
+    (dict(k=0x1000000), 1), (dict(k_scale=0x4000000), 1), (dict(lens=0x1000000), 1),
+])
+def test_cache_store_refusals(kw, code):
+    st, msg = _call("gdn_cache_store", block.CacheStoreArgs, STORE, kw)
+    assert st == code and msg.startswith("gdn_cache_store"), msg
+
+
+@pytest.mark.parametrize("kw,code", POOL_BAD + [
+    (dict(h_q=3), 1), (dict(h_q=0), 1), (dict(causal=2), 1), (dict(window=-1), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1),
+    (dict(scale=float("inf")), 1), (dict(q=0), 1), (dict(o=0), 1), (dict(q_stride=255), 1), (dict(o_stride=260), 3), (dict(gate=0x30008), 3),
+    (dict(o=0x10010), 1), (dict(lse=0x80002), 3), (dict(lse=0x20000), 1), (dict(gate=0x20000), 1), (dict(o=0x1000000), 1),
+    (dict(max_pages=4096), 4), (dict(max_pages=4096, workspace=0x7000001, workspace_bytes=1 << 30), 3),
+    (dict(max_pages=4096, workspace=0x1000000, workspace_bytes=1 << 30), 1),
+])
+def test_cache_attention_refusals(kw, code):
+    st, msg = _call("gdn_cache_attention", block.CacheAttentionArgs, ATTEND, kw)
+    assert st == code and msg.startswith("gdn_cache_attention"), msg
+
+
+def test_cache_attention_workspace():
+    size = gdn.cache_attention_workspace_size
+    assert size(1, 1, 1, 24, 4, 256) == 0  # one piece: nothing to join
+    assert size(64, 64, 512, 24, 4, 256) > 0
+    assert size(0, 1, 512, 24, 4, 256) == 0
+    assert size(1, 1, 512, 23, 4, 256) == 0  # invalid
+
+
+def test_rope_frequencies():
+    import math
+
+    import torch
+
+    f, m = gdn.rope_frequencies(64, 1e4)
+    assert f.dtype == torch.float64 and m == 1.0 and f[0] == 1.0 and math.isclose(f[31].item(), 1e4 ** (-62 / 64))
+    g, _ = gdn.rope_frequencies(64, 1e4, "linear", 4.0)
+    assert torch.allclose(g, f / 4)
+    g, _ = gdn.rope_frequencies(64, 1e4, "ntk", 4.0)
+    assert g[0] == 1.0 and math.isclose(g[31].item(), f[31].item() / 4)
+    g, m = gdn.rope_frequencies(64, 1e4, "by_parts", 4.0, original=4096)
+    assert g[0] == f[0] and math.isclose(g[31].item(), f[31].item() / 4) and math.isclose(m, 0.1 * math.log(4) + 1)
+    assert ((g <= f) & (g >= f / 4)).all()
+    for bad in (dict(rot=3), dict(rot=0), dict(rot=8, scaling="other"), dict(rot=8, scaling="by_parts"), dict(rot=8, factor=0.5)):
+        with pytest.raises(gdn.GdnError):
+            gdn.rope_frequencies(**bad)
