@@ -38,6 +38,9 @@
 #include "gdn_device.h"
 #include "gdn_internal.h"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace gdn {
 namespace {
 
@@ -110,6 +113,7 @@ struct Tile {
   int len;         // new tokens
   int ctx;         // tokens in the cache, the new ones among them
   int lo, hi;      // keys, lo a multiple of kTok
+  int all_lo, all_hi;  // keys that every row sees
   bool some;       // whether there is such a tile
 };
 
@@ -141,6 +145,8 @@ __device__ __forceinline__ Tile find_tile(const AttendParams& p, int slot, int g
   if (!t.some) return t;
   const int t0 = t.first / group, t1 = min(t.len - 1, (t.first + tile_rows - 1) / group);
   t.hi = p.causal ? min(t.ctx, t.ctx - t.len + t1 + 1) : t.ctx;
+  t.all_hi = p.causal ? min(t.ctx, t.ctx - t.len + t0 + 1) : t.ctx;
+  t.all_lo = p.window ? t.ctx - t.len + t1 - p.window + 1 : 0;
   t.lo = p.window ? max(0, t.ctx - t.len + t0 - p.window + 1) : 0;
   t.lo &= ~(kTok - 1);
   if (t.hi < t.lo) t.hi = t.lo;
@@ -157,11 +163,40 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return (~m & 0x80808080u) >> 7;                                      // 1 where NaN
 }
 
+// A mask of the first n of 8 codes.
+__device__ __forceinline__ uint2 first_codes(int n) {
+  return make_uint2(n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1, n >= 8 ? 0xffffffffu : n <= 4 ? 0u : (1u << (8 * (n - 4))) - 1);
+}
+// NaN for the rows that see a NaN among 8 values of each lane: a product of ones
+// (a code is NaN) and ones (the row sees tokens from .. to - 1).  0x38 is e4m3's 1.
 template <typename T>
-__device__ __forceinline__ float gated(const AttendParams& p, float o, int64_t token, int64_t at) {
-  if (!p.gate) return o;
-  const float z = to_f32(reinterpret_cast<const T*>(p.gate)[token * p.gate_stride + at]);
-  return o / (1.f + (sizeof(T) == 2 ? __expf(-z) : expf(-z)));
+__device__ __forceinline__ void give_nan(uint2 nan, int from, int to, f32x4& o) {
+  typedef Probs<T> P;
+  float one[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) one[e] = e >= from && e < to ? 1.f : 0.f;
+  typename P::vec see[P::N];
+  P::make(one, see);
+  const f32x4 hit = mfma(P::codes(nan.x * 0x38u, nan.y * 0x38u), see[0], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = hit[e] > 0.f ? __builtin_nanf("") : o[e];
+}
+
+// y * sigmoid(z)
+template <typename T>
+__device__ __forceinline__ float gated(float y, float z) { return y / (1.f + (sizeof(T) == 2 ? __expf(-z) : expf(-z))); }
+
+// Four elements of an output row, gated where there is a gate.
+template <typename T>
+__device__ __forceinline__ void put(const AttendParams& p, f32x4 o, int64_t token, int64_t at) {
+  float y[4] = {o[0], o[1], o[2], o[3]};
+  if (p.gate) {
+    float z[4];
+    load4(reinterpret_cast<const T*>(p.gate) + token * p.gate_stride + at, z);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = gated<T>(y[e], z[e]);
+  }
+  store4(reinterpret_cast<T*>(p.o) + token * p.o_stride + at, y);
 }
 
 template <typename T, int D>
@@ -286,39 +321,20 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
     l = l * alpha + sum;
 
     if (part) {
-      // codes that must not reach the product: tokens behind the context, or of no page
-      const int keep = held ? max(0, min(tile.ctx - ts, 16)) : 0;
-      uint32_t mask[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = keep - 4 * i;
-        mask[i] = k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1;
-      }
-      uint32_t bad = 0;
+      // codes that must not reach the product: tokens behind the context or of no page, and NaN
+      const int n = held ? tile.ctx - ts : 0;
+      const uint2 keep[2] = {first_codes(n), first_codes(n - 8)};
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        vc[i].x &= mask[0]; vc[i].y &= mask[1]; vc[i].z &= mask[2]; vc[i].w &= mask[3];
-        bad |= nan_bytes(vc[i].x) | nan_bytes(vc[i].y) | nan_bytes(vc[i].z) | nan_bytes(vc[i].w);
-      }
-      if (__any(bad != 0)) {
-        // NaN codes leave the product; rows that see one get NaN there, by a product of
-        // ones (a code is NaN) and ones (a row sees the token)
-        float one[2][8];
+        uint32_t* c = reinterpret_cast<uint32_t*>(&vc[i]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) one[e >> 3][e & 7] = e >= from && e < to ? 1.f : 0.f;
-        typename P::vec see[2][P::N];
-        P::make(one[0], see[0]);
-        P::make(one[1], see[1]);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const uint4 c = vc[i];
-          const uint4 nn = make_uint4(nan_bytes(c.x), nan_bytes(c.y), nan_bytes(c.z), nan_bytes(c.w));
-          f32x4 hit = f32x4{0.f, 0.f, 0.f, 0.f};
-          hit = mfma(P::codes(nn.x * 0x38u, nn.y * 0x38u), see[0][0], hit);  // 0x38: 1.0
-          hit = mfma(P::codes(nn.z * 0x38u, nn.w * 0x38u), see[1][0], hit);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] = hit[e] > 0.f ? __builtin_nanf("") : o[i][e];
-          vc[i] = make_uint4(c.x & ~(nn.x * 0xffu), c.y & ~(nn.y * 0xffu), c.z & ~(nn.z * 0xffu), c.w & ~(nn.w * 0xffu));
+        for (int u = 0; u < 2; ++u) {
+          c[2 * u] &= keep[u].x, c[2 * u + 1] &= keep[u].y;
+          const uint2 bad = make_uint2(nan_bytes(c[2 * u]), nan_bytes(c[2 * u + 1]));
+          if (__any((bad.x | bad.y) != 0)) {
+            give_nan<T>(bad, from - 8 * u, to - 8 * u, o[i]);
+            c[2 * u] &= ~(bad.x * 0xffu), c[2 * u + 1] &= ~(bad.y * 0xffu);
+          }
         }
       }
     }
@@ -364,10 +380,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
     const int64_t out = token * p.h_q + h;
     if (ns == 1) {
       const float inv = ll == 0.f ? 0.f : 1.f / ll;
-      float y[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = gated<T>(p, sum[e] * inv, token, (int64_t)h * D + c + e);
-      store4(reinterpret_cast<T*>(p.o) + token * p.o_stride + (int64_t)h * D + c, y);
+      put<T>(p, sum * inv, token, (int64_t)h * D + c);
       if (p.lse && c == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (mm + __log2f(ll)) * 0.69314718055994530942f;
     } else {
       const int64_t part = (int64_t)piece * p.tokens * p.h_q + out;
@@ -377,15 +390,365 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
   }
 }
 
+// Long chunks: a workgroup's four waves take NT * 16 rows each against the same
+// keys and values.  A tile of 64 tokens, codes as they are, goes from memory
+// to LDS without passing registers, one tile ahead of the products (two
+// buffers, one barrier a tile); every wave turns the codes it reads into
+// operands.  Sixteen-byte pieces are stored at places exclusive-ored with their
+// row, so that the 16 rows that one read takes lie in different banks.
+#ifndef NT256
+#define NT256 2
+#endif
+template <typename T, int D>
+constexpr int kRowTiles = (sizeof(T) == 2 ? 2 : 1) * (D == 256 && sizeof(T) == 2 ? NT256 / 2 : 1);  // NT: fp32 rows take three registers where bf16 rows take one
+template <typename T, int D>
+constexpr int kChunkRows = kWaves * kRows * kRowTiles<T, D>;
+inline int chunk_rows(bool bf16, int d) {
+  return kWaves * kRows * (bf16 ? d == 256 ? kRowTiles<__bf16, 256> : kRowTiles<__bf16, 128> : kRowTiles<float, 256>);
+}
+
+// 16 bytes a lane from src + AT to dst + AT + 16 lane (dst: the wave's).
+template <int AT>
+__device__ __forceinline__ void to_lds(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)src,
+                                   (__attribute__((address_space(3))) uint32_t*)dst, 16, AT, 0);
+}
+// The least and the largest of a wave's values, in a scalar register.
+__device__ __forceinline__ int wave_min(int v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v = min(v, __shfl_xor(v, m, 64));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+__device__ __forceinline__ int wave_max(int v) { return -wave_min(-v); }
+
+// What a tile of 64 tokens needs besides codes, for its four groups of 16 tokens (one where a page holds the
+// whole tile): uniform, in scalar registers.
+template <bool ONE>
+struct TilePages {
+  static constexpr int N = ONE ? 1 : 4;
+  int id[N];
+  float ks[N], vs[N];
+  template <typename V>
+  static __device__ __forceinline__ V of(const V (&v)[N], int g) {
+    if constexpr (ONE) {
+      return v[0];
+    } else {
+      const V lo = g & 1 ? v[1] : v[0], hi = g & 1 ? v[3] : v[2];
+      return g & 2 ? hi : lo;
+    }
+  }
+};
+
+// ONE: a page holds at least 64 tokens.
+template <typename T, int D, bool ONE>
+__global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendParams p) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int NQ = F32 ? 3 : 1, NT = kRowTiles<T, D>;
+  constexpr int KS = D / 32, MT = D / 16, RS = D == 256 ? 0 : D == 128 ? 1 : 2;
+  constexpr int kBytes = 2 * kTok * D;  // a tile: keys, then values
+  typedef Probs<T> P;
+  __shared__ alignas(16) uint8_t tiles[2 * kBytes];
+
+  const int group = p.h_q / p.h_kv;
+  const int head = blockIdx.y, piece = blockIdx.z;
+  // later tiles see more keys: they begin first
+  const Tile tile = find_tile(p, gridDim.x - 1 - blockIdx.x, group, kChunkRows<T, D>);
+  if (!tile.some) return;
+  const int ns = pieces(p, tile);
+  if (piece >= ns) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+
+  int row_lo[NT], row_hi[NT];
+  bf16x8 q[NT][KS][NQ];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row = tile.first + (wave * NT + t) * kRows + r;
+    const bool live = row < tile.rows;
+    const int tok = row / group, hq = head * group + (row - tok * group);
+    const int pos = tile.ctx - tile.len + tok;
+    row_hi[t] = live ? (p.causal ? min(tile.ctx, pos + 1) : tile.ctx) : 0;
+    row_lo[t] = live && p.window ? pos - p.window + 1 : 0;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int at = (k / 2) * 64 + g * 16 + (k & 1) * 8;
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (live) load8(reinterpret_cast<const T*>(p.q) + (tile.begin + tok) * p.q_stride + (int64_t)hq * D + at, f);
+      if constexpr (F32) {
+        split3_any(f, q[t][k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[t][k][0][i] = (__bf16)f[i];
+      }
+    }
+  }
+  f32x4 o[NT][MT];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = -__builtin_inff();
+    l[t] = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // what all of this wave's rows see, and what any of them does
+  int all_lo = 0, all_hi = INT32_MAX, any_lo = INT32_MAX, any_hi = 0;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const bool live = row_hi[t] > 0;
+    all_lo = max(all_lo, live ? row_lo[t] : 0);
+    all_hi = min(all_hi, live ? row_hi[t] : INT32_MAX);
+    any_lo = min(any_lo, live ? row_lo[t] : INT32_MAX);
+    any_hi = max(any_hi, row_hi[t]);
+  }
+  all_lo = wave_max(all_lo), all_hi = wave_min(all_hi), any_lo = wave_min(any_lo), any_hi = wave_max(any_hi);
+
+  const int start = tile.lo + piece * p.piece;
+  const int stop = min(tile.hi, start + p.piece);
+  const int in_page = (1 << p.page_shift) - 1;
+  typedef TilePages<ONE> Pages;
+  cint32* table = as_const(p.page_table + (int64_t)tile.n * p.max_pages);
+  const __attribute__((address_space(4))) float* k_scale = (const __attribute__((address_space(4))) float*)(p.k_scale);
+  const __attribute__((address_space(4))) float* v_scale = (const __attribute__((address_space(4))) float*)(p.v_scale);
+  auto inside = [&](int id) { return id >= 0 && id < p.pages ? id : 0; };
+  // (a group behind the last token takes the last token's page: its scores are masked)
+  auto pages_of = [&](int k0, Pages& t) {
+#pragma unroll
+    for (int j = 0; j < Pages::N; ++j) t.id[j] = table[min(k0 + 16 * j, stop - 1) >> p.page_shift];
+  };
+  auto scales_of = [&](Pages& t) {
+#pragma unroll
+    for (int j = 0; j < Pages::N; ++j) {
+      const int64_t at = (int64_t)inside(t.id[j]) * p.h_kv + head;
+      t.ks[j] = k_scale[at];
+      t.vs[j] = v_scale[at];
+    }
+  };
+  // this lane's part of the tile's copy: keys of the 16 tokens of group `wave`, values of the tokens of group vg
+  const int vg = (lane & 3) ^ (lane >> 4);
+  const int krow = lane / (D / 16);
+  const int k_from = krow * D + (((lane % (D / 16)) ^ (((krow & 3) | (wave << 2)) >> RS)) * 16);
+  const int v_from = ((lane >> 2) << p.page_shift) + (ONE ? 16 * vg : 0);
+  auto stage = [&](int half, int k0, const Pages& t) {
+    uint8_t* dst = tiles + half * kBytes + wave * (D * 16);
+    const uint8_t* ks = p.k_cache + ((((int64_t)inside(Pages::of(t.id, wave)) * p.h_kv + head) << p.page_shift) + ((k0 + 16 * wave) & in_page)) * D;
+    const uint8_t* vs = p.v_cache + ((((int64_t)inside(Pages::of(t.id, vg)) * p.h_kv + head) * D + wave * (D / 4)) << p.page_shift) +
+                        ((k0 + (ONE ? 0 : 16 * vg)) & in_page);
+    auto copy = [&](auto J) {
+      constexpr int j = decltype(J)::value;
+      to_lds<j * 1024>(ks + k_from, dst);
+      to_lds<0>(vs + v_from + ((16 * j) << p.page_shift), dst + kTok * D + j * 1024);
+    };
+    copy(std::integral_constant<int, 0>{});
+    if constexpr (D > 64) copy(std::integral_constant<int, 1>{});
+    if constexpr (D > 128) copy(std::integral_constant<int, 2>{}), copy(std::integral_constant<int, 3>{});
+  };
+
+  const int key_at = (16 * (r >> 2) + (r & 3)) * D + ((g ^ (r >> RS)) * 16);
+  const int value_at = kTok * D + r * 64 + ((g ^ (r >> 2)) * 16);
+  // A tile that some row of the workgroup does not see whole: codes that must not reach the products are cleared
+  // in LDS, those of tokens behind the context or of no page, and NaN (which the rows that see one get here).
+  auto clear = [&](int half, int k0, const Pages& pages) {
+    uint8_t* values = tiles + half * kBytes + kTok * D;
+    uint32_t bad = 0;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < 4 * D; i += kWaves * 64) {
+      const int of = (i & 3) ^ ((i >> 4) & 3), id = Pages::of(pages.id, of);
+      const int n = id >= 0 && id < p.pages ? tile.ctx - k0 - 16 * of : 0;
+      uint4* at = reinterpret_cast<uint4*>(values + i * 16);
+      uint4 c = *at;
+      const uint2 a = first_codes(n), b = first_codes(n - 8);
+      c = make_uint4(c.x & a.x, c.y & a.y, c.z & b.x, c.w & b.y);
+      bad |= nan_bytes(c.x) | nan_bytes(c.y) | nan_bytes(c.z) | nan_bytes(c.w);
+      *at = c;
+    }
+    if (!__syncthreads_or(bad != 0)) return;
+    const int ts = k0 + 16 * g;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint2 c = *reinterpret_cast<const uint2*>(tiles + half * kBytes + value_at + i * 1024 + 8 * u);
+        const uint2 nan = make_uint2(nan_bytes(c.x), nan_bytes(c.y));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          give_nan<T>(nan, row_lo[t] - ts - 8 * u, row_hi[t] - ts - 8 * u, o[t][i]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < 16 * D; i += kWaves * 64) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(values + i * 4);
+      *at &= ~(nan_bytes(*at) * 0xffu);
+    }
+    __syncthreads();
+  };
+
+  // whole: every row of the wave sees every token of the tile
+  auto compute = [&](bool whole, int half, int k0, const Pages& pages) {
+    const int ts = k0 + 16 * g;
+    const int id = Pages::of(pages.id, g);
+    const bool held = id >= 0 && id < p.pages;
+    // (a scale of zero: scores of zero, and no 0 * infinity where they are masked)
+    const float unit = Pages::of(pages.ks, g) * p.scale_log2, f = held ? (unit == 0.f ? 1e-30f : unit) : 1.f;
+    // vs enters the weights' exponent; the sum takes it back out.  Beyond 2^-40 .. 2^120 a factor is left over.
+    const float vs = held ? Pages::of(pages.vs, g) : 1.f;
+    const float lv = fminf(fmaxf(__log2f(fabsf(vs)), -40.f), 120.f);
+    const float back = __builtin_amdgcn_exp2f(-lv);
+    const bool wild = __any(!(vs >= 0x1p-40f && vs <= 0x1p120f));
+    // Half a tile a turn (tokens 16 g + 8 u .. + 7 of every group): its scores are half the registers
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+      f32x4 s[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int keys = half * kBytes + 8 * u * D + key_at;
+      auto key = [&](int b, int h) { return *reinterpret_cast<const uint4*>(tiles + (keys ^ (b * 64)) + 4 * h * D); };
+      uint4 c[2] = {key(0, 0), key(0, 1)};
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
+        uint4 next[2];
+        if (b + 1 < D / 64) next[0] = key(b + 1, 0), next[1] = key(b + 1, 1);
+#pragma unroll
+        for (int i2 = 0; i2 < 4; ++i2) {
+          const int h = i2 & 1, hi = i2 >> 1;
+          const bf16x8 kk = hi ? to_bf16x8(c[h].z, c[h].w) : to_bf16x8(c[h].x, c[h].y);
+#pragma unroll
+          for (int i = NQ - 1; i >= 0; --i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[t][h] = mfma(kk, q[t][2 * b + hi][i], s[t][h]);
+        }
+        if (b + 1 < D / 64) c[0] = next[0], c[1] = next[1];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int lo = row_lo[t] - ts - 8 * u, hi = held ? row_hi[t] - ts - 8 * u : 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < lo || e >= hi) s[t][e >> 2][e & 3] = -__builtin_inff();
+        }
+      }
+
+      typename P::vec pw[NT][P::N];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float top = s[t][0][0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[t][e >> 2][e & 3]);
+        top = fmaf(top, f, lv);
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        // the maximum moves only where it grows by more than 2^8: the weights then stay under 256
+        if (__any(top > m[t] + 8.f)) {
+          const float now = fmaxf(m[t], top);
+          const float alpha = now == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m[t] - now);
+          m[t] = now;
+          l[t] *= alpha;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) o[t][i] *= alpha;
+        }
+        const float base = lv - (m[t] == -__builtin_inff() ? 0.f : m[t]);
+        float w[8], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          w[e] = __builtin_amdgcn_exp2f(fmaf(s[t][e >> 2][e & 3], f, base));
+          sum += w[e];
+        }
+        l[t] = fmaf(sum, back, l[t]);
+        if (wild) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] *= vs * back;
+        }
+        P::make(w, pw[t]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+
+      const int values = half * kBytes + 8 * u + value_at;
+      auto value = [&](int i) { return *reinterpret_cast<const uint2*>(tiles + values + i * 1024); };
+      uint2 v[2] = {value(0), value(1)};
+#pragma unroll
+      for (int i = 0; i < MT; i += 2) {
+        uint2 next[2];
+        if (i + 2 < MT) next[0] = value(i + 2), next[1] = value(i + 3);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const typename P::vec vv = P::codes(v[h].x, v[h].y);
+#pragma unroll
+          for (int e = P::N - 1; e >= 0; --e)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[t][i + h] = mfma(vv, pw[t][e], o[t][i + h]);
+        }
+        if (i + 2 < MT) v[0] = next[0], v[1] = next[1];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+
+  // A turn: the tile's codes have come (every wave waits for its own, then for the others'), the next tile's are
+  // asked for, and the tile is worked through.
+  Pages here, next;
+  if (start < stop) {
+    pages_of(start, here);
+    stage(0, start, here);
+    scales_of(here);
+    pages_of(start + kTok, next);
+  }
+  int half = 0;
+#pragma unroll 1
+  for (int k0 = start; k0 < stop; k0 += kTok) {
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __syncthreads();
+    if (k0 + kTok < stop) {
+      stage(half ^ 1, k0 + kTok, next);
+      scales_of(next);
+    }
+    bool there = true;
+#pragma unroll
+    for (int j = 0; j < Pages::N; ++j) there = there && here.id[j] >= 0 && here.id[j] < p.pages;
+    if (!(there && k0 >= tile.all_lo && k0 + kTok <= tile.all_hi)) clear(half, k0, here);
+    if (k0 < any_hi && k0 + kTok > any_lo) compute(there && k0 >= all_lo && k0 + kTok <= all_hi, half, k0, here);
+    here = next;
+    pages_of(k0 + 2 * kTok, next);
+    half ^= 1;
+  }
+
+  int row0 = tile.first + wave * (NT * kRows) + r;
+  asm volatile("" : "+v"(row0));  // worked out here, not kept through the loop
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row = row0 + t * kRows;
+    l[t] += __shfl_xor(l[t], 16, 64);
+    l[t] += __shfl_xor(l[t], 32, 64);
+    if (row >= tile.rows) continue;
+    const int64_t token = tile.begin + row / group;
+    const int h = head * group + row % group;
+    const int64_t out = token * p.h_q + h;
+    if (ns == 1) {
+      const float inv = l[t] == 0.f ? 0.f : 1.f / l[t];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) put<T>(p, o[t][i] * inv, token, (int64_t)h * D + i * 16 + g * 4);
+      if (p.lse && g == 0) p.lse[out] = l[t] == 0.f ? -__builtin_inff() : (m[t] + __log2f(l[t])) * 0.69314718055994530942f;
+    } else {
+      const int64_t part = (int64_t)piece * p.tokens * p.h_q + out;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(p.part_o + part * D + i * 16 + g * 4) = o[t][i];
+      if (g == 0) p.part_ml[2 * part] = m[t], p.part_ml[2 * part + 1] = l[t];
+    }
+  }
+}
+
 // Joins the pieces of a row: a wave a row, its lanes over the head's elements.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_kernel(AttendParams p) {
   const int group = p.h_q / p.h_kv, lane = threadIdx.x & 63;
-  const Tile tile = find_tile(p, blockIdx.x, group, kRows);
+  const Tile tile = find_tile(p, blockIdx.x, group, p.tile_rows);
   if (!tile.some) return;
   const int ns = pieces(p, tile);
   if (ns == 1) return;  // written already
-  for (int rr = threadIdx.x >> 6; rr < kRows; rr += 4) {
+  for (int rr = threadIdx.x >> 6; rr < p.tile_rows; rr += 4) {
     const int at = tile.first + rr;
     if (at >= tile.rows) return;
     const int64_t token = tile.begin + at / group;
@@ -409,7 +772,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttendParams p) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int64_t c = (int64_t)h * D + e * 64 + lane;
-      reinterpret_cast<T*>(p.o)[token * p.o_stride + c] = from_f32<T>(gated<T>(p, sum[e] * inv, token, c));
+      float y = sum[e] * inv;
+      if (p.gate) y = gated<T>(y, to_f32(reinterpret_cast<const T*>(p.gate)[token * p.gate_stride + c]));
+      reinterpret_cast<T*>(p.o)[token * p.o_stride + c] = from_f32<T>(y);
     }
     if (p.lse && lane == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (mm + __log2f(ll)) * 0.69314718055994530942f;
   }
@@ -417,6 +782,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttendParams p) {
 
 // How a call is cut: tiles of rows, and pieces of the context of `piece` tokens.
 struct Plan {
+  bool chunk;      // attend_chunk_kernel
+  int32_t tile_rows;
   int64_t slots;  // tiles at most
   int32_t uniform_tiles;
   int64_t uniform;
@@ -434,13 +801,17 @@ Plan plan(const AttendShape& a) {
   Plan c;
   const int64_t group = a.h_q / a.h_kv;
   c.uniform = a.tokens / a.n_seqs;
-  c.uniform_tiles = (int32_t)((c.uniform * group + kRows - 1) / kRows);
-  c.slots = a.ragged ? a.tokens * group / kRows + a.n_seqs : (int64_t)c.uniform_tiles * a.n_seqs;
+  // Sequences of 64 rows and more on average share their keys among a workgroup's waves.
+  c.chunk = a.tokens * group >= (int64_t)a.n_seqs * 64;
+  c.tile_rows = !c.chunk ? kRows : chunk_rows(a.bf16, a.d);
+  c.uniform_tiles = (int32_t)((c.uniform * group + c.tile_rows - 1) / c.tile_rows);
+  c.slots = a.ragged ? a.tokens * group / c.tile_rows + a.n_seqs : (int64_t)c.uniform_tiles * a.n_seqs;
   // Pieces: about 4096 workgroups where the contexts allow it (16 for each CU: unequal contexts then even
-  // out), of at least 256 tokens, a turn of a workgroup's four waves.
-  const int64_t most = max_tokens(a), step = kWaves * kTok;
-  const double even = (double)most * a.h_kv * c.slots / 4096;
-  int64_t piece = even >= (double)most ? most : (int64_t)even;
+  // out), of at least 256 tokens, a turn of a workgroup's four waves.  Chunks: about 1024 where there are
+  // fewer than 512 without pieces, of at least 512 tokens.
+  const int64_t most = max_tokens(a), step = c.chunk ? 512 : kWaves * kTok, tiles = c.slots * a.h_kv;
+  int64_t piece = most;
+  if (!c.chunk || tiles < 512) piece = (int64_t)std::min((double)most, (double)most * tiles / (c.chunk ? 1024 : 4096));
   piece = (piece + step - 1) / step * step;
   c.piece = (int32_t)(piece < step ? step : piece);
   c.pieces = (most + c.piece - 1) / c.piece;
@@ -450,8 +821,10 @@ Plan plan(const AttendShape& a) {
 
 template <typename T, int D>
 hipError_t launch(AttendParams p, const Plan& c, hipStream_t stream) {
-  hipLaunchKernelGGL((attend_kernel<T, D>), dim3((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)c.pieces), dim3(kWaves * 64), 0,
-                     stream, p);
+  const dim3 grid((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)c.pieces);
+  if (c.chunk && p.page_shift >= 6) hipLaunchKernelGGL((attend_chunk_kernel<T, D, true>), grid, dim3(kWaves * 64), 0, stream, p);
+  else if (c.chunk) hipLaunchKernelGGL((attend_chunk_kernel<T, D, false>), grid, dim3(kWaves * 64), 0, stream, p);
+  else hipLaunchKernelGGL((attend_kernel<T, D>), grid, dim3(kWaves * 64), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || c.pieces == 1) return e;
   hipLaunchKernelGGL((join_kernel<T, D>), dim3((unsigned)c.slots, (unsigned)p.h_kv), dim3(256), 0, stream, p);
@@ -486,6 +859,7 @@ hipError_t launch_attend(AttendParams p, const AttendShape& a, void* workspace, 
   p.uniform = c.uniform;
   p.uniform_tiles = c.uniform_tiles;
   p.piece = c.piece;
+  p.tile_rows = c.tile_rows;
   if (c.pieces > 1) {
     const size_t rows = (size_t)c.pieces * a.tokens * a.h_q;
     p.part_o = reinterpret_cast<float*>(workspace);

@@ -264,6 +264,7 @@ struct AttendShape {
   int32_t page;
   int32_t max_pages;
   int32_t ragged;
+  int32_t bf16;
 };
 struct AttendParams {
   const void* q;
@@ -295,6 +296,7 @@ struct AttendParams {
   int32_t uniform_tiles;
   int64_t uniform;
   int32_t piece;
+  int32_t tile_rows;
   float* part_o;   // [pieces, tokens, h_q, d]
   float* part_ml;  // [pieces, tokens, h_q, 2]
 };
