@@ -38,6 +38,7 @@
 #include "gdn_device.h"
 #include "gdn_internal.h"
 
+#include <cstdlib>
 #include <algorithm>
 #include <type_traits>
 
@@ -85,6 +86,14 @@ __device__ __forceinline__ void split3_any(const float (&f)[8], bf16x8 (&out)[3]
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// The largest of the four lanes r, r + 16, r + 32, r + 48, for each of them.
+__device__ __forceinline__ float group_max(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
 
 // The probabilities' operand and the values' type that goes with it.
 template <typename T> struct Probs;
@@ -592,11 +601,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendPara
     const bool held = id >= 0 && id < p.pages;
     // (a scale of zero: scores of zero, and no 0 * infinity where they are masked)
     const float unit = Pages::of(pages.ks, g) * p.scale_log2, f = held ? (unit == 0.f ? 1e-30f : unit) : 1.f;
-    // vs enters the weights' exponent; the sum takes it back out.  Beyond 2^-40 .. 2^120 a factor is left over.
     const float vs = held ? Pages::of(pages.vs, g) : 1.f;
     const float lv = fminf(fmaxf(__log2f(fabsf(vs)), -40.f), 120.f);
-    const float back = __builtin_amdgcn_exp2f(-lv);
-    const bool wild = __any(!(vs >= 0x1p-40f && vs <= 0x1p120f));
     // Half a tile a turn (tokens 16 g + 8 u .. + 7 of every group): its scores are half the registers
 #pragma unroll 1
     for (int u = 0; u < 2; ++u) {
@@ -610,6 +616,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendPara
       for (int b = 0; b < D / 64; ++b) {
         uint4 next[2];
         if (b + 1 < D / 64) next[0] = key(b + 1, 0), next[1] = key(b + 1, 1);
+        __builtin_amdgcn_sched_barrier(0);  // asked for before this step's products, not where registers come free
 #pragma unroll
         for (int i2 = 0; i2 < 4; ++i2) {
           const int h = i2 & 1, hi = i2 >> 1;
@@ -632,56 +639,64 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendPara
         }
       }
 
-      typename P::vec pw[NT][P::N];
+      float top[NT];
+      bool grows = false;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float top = s[t][0][0];
+        top[t] = s[t][0][0];
 #pragma unroll
-        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[t][e >> 2][e & 3]);
-        top = fmaf(top, f, lv);
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        // the maximum moves only where it grows by more than 2^8: the weights then stay under 256
-        if (__any(top > m[t] + 8.f)) {
-          const float now = fmaxf(m[t], top);
+        for (int e = 1; e < 8; ++e) top[t] = fmaxf(top[t], s[t][e >> 2][e & 3]);
+        top[t] = group_max(fmaf(top[t], f, lv));
+        grows = grows || top[t] > m[t] + 8.f;
+      }
+      // the maximum moves only where it grows by more than 2^8: the weights then stay under 256
+      if (__any(grows)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float now = fmaxf(m[t], top[t]);
           const float alpha = now == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m[t] - now);
           m[t] = now;
           l[t] *= alpha;
 #pragma unroll
           for (int i = 0; i < MT; ++i) o[t][i] *= alpha;
         }
-        const float base = lv - (m[t] == -__builtin_inff() ? 0.f : m[t]);
-        float w[8], sum = 0.f;
+      }
+      typename P::vec pw[NT][P::N];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
+        float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          w[e] = __builtin_amdgcn_exp2f(fmaf(s[t][e >> 2][e & 3], f, base));
-          sum += w[e];
-        }
-        l[t] = fmaf(sum, back, l[t]);
-        if (wild) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] *= vs * back;
+          w[e] = __builtin_amdgcn_exp2f(fmaf(s[t][e >> 2][e & 3], f, -base));
+          l[t] += w[e];
+          w[e] *= vs;
         }
         P::make(w, pw[t]);
       }
-      __builtin_amdgcn_sched_barrier(0);
 
       const int values = half * kBytes + 8 * u + value_at;
       auto value = [&](int i) { return *reinterpret_cast<const uint2*>(tiles + values + i * 1024); };
-      uint2 v[2] = {value(0), value(1)};
+      uint2 v[4] = {value(0), value(1), value(2), value(3)};
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < MT; i += 2) {
-        uint2 next[2];
-        if (i + 2 < MT) next[0] = value(i + 2), next[1] = value(i + 3);
+      for (int i = 0; i < MT; i += 4) {
+        uint2 next[4];
+        if (i + 4 < MT)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 4; ++h) next[h] = value(i + 4 + h);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
           const typename P::vec vv = P::codes(v[h].x, v[h].y);
 #pragma unroll
           for (int e = P::N - 1; e >= 0; --e)
 #pragma unroll
             for (int t = 0; t < NT; ++t) o[t][i + h] = mfma(vv, pw[t][e], o[t][i + h]);
         }
-        if (i + 2 < MT) v[0] = next[0], v[1] = next[1];
+        if (i + 4 < MT)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) v[h] = next[h];
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -813,6 +828,7 @@ Plan plan(const AttendShape& a) {
   int64_t piece = most;
   if (!c.chunk || tiles < 512) piece = (int64_t)std::min((double)most, (double)most * tiles / (c.chunk ? 1024 : 4096));
   piece = (piece + step - 1) / step * step;
+  if (c.chunk) if (const char* e = getenv("XPIECE")) piece = atoi(e);
   c.piece = (int32_t)(piece < step ? step : piece);
   c.pieces = (most + c.piece - 1) / c.piece;
   if (c.pieces < 1) c.pieces = 1;
