@@ -399,21 +399,36 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
   }
 }
 
-// Long chunks: a workgroup's four waves take NT * 16 rows each against the same
+// Long chunks: a workgroup's four waves take 32 rows each against the same
 // keys and values.  A tile of 64 tokens, codes as they are, goes from memory
 // to LDS without passing registers, one tile ahead of the products (two
 // buffers, one barrier a tile); every wave turns the codes it reads into
-// operands.  Sixteen-byte pieces are stored at places exclusive-ored with their
-// row, so that the 16 rows that one read takes lie in different banks.
-#ifndef NT256
-#define NT256 2
-#endif
-template <typename T, int D>
-constexpr int kRowTiles = (sizeof(T) == 2 ? 2 : 1) * (D == 256 && sizeof(T) == 2 ? NT256 / 2 : 1);  // NT: fp32 rows take three registers where bf16 rows take one
-template <typename T, int D>
-constexpr int kChunkRows = kWaves * kRows * kRowTiles<T, D>;
-inline int chunk_rows(bool bf16, int d) {
-  return kWaves * kRows * (bf16 ? d == 256 ? kRowTiles<__bf16, 256> : kRowTiles<__bf16, 128> : kRowTiles<float, 256>);
+// operands.  The products are 32x32x16 MFMAs: an MFMA of either size keeps
+// vector instructions from issuing for about 8 of its cycles, and the larger
+// one has twice as many to give.  Half a tile's scores S^T are 16 registers: a
+// lane (row c, half h) holds those of 16 neighbouring tokens again, as keys
+// are dealt to the operand's rows as token 16 (m >> 2 & 1) + 4 (m >> 3) + (m & 3).
+// Sixteen-byte pieces are stored at places exclusive-ored with their row, so
+// that the 16 rows that one read takes lie in different banks.
+constexpr int kChunkRows = kWaves * 32;
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f32x16 zeros16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+// The larger of lanes l and l ^ 32.
+__device__ __forceinline__ float half_max(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 
 // 16 bytes a lane from src + AT to dst + AT + 16 lane (dst: the wave's).
@@ -450,67 +465,66 @@ struct TilePages {
 
 // ONE: a page holds at least 64 tokens.
 template <typename T, int D, bool ONE>
-__global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendParams p) {
+__global__ __launch_bounds__(kWaves * 64, sizeof(T) == 4 && D == 256 ? 1 : 2) void attend_chunk_kernel(AttendParams p) {
   constexpr bool F32 = sizeof(T) == 4;
-  constexpr int NQ = F32 ? 3 : 1, NT = kRowTiles<T, D>;
-  constexpr int KS = D / 32, MT = D / 16, RS = D == 256 ? 0 : D == 128 ? 1 : 2;
+  constexpr int NQ = F32 ? 3 : 1;
+  constexpr int KB = D / 32, MT = D / 32, RS = D == 256 ? 0 : D == 128 ? 1 : 2;
   constexpr int kBytes = 2 * kTok * D;  // a tile: keys, then values
   typedef Probs<T> P;
   __shared__ alignas(16) uint8_t tiles[2 * kBytes];
 
   const int group = p.h_q / p.h_kv;
-  const int head = blockIdx.y, piece = blockIdx.z;
-  // later tiles see more keys: they begin first
-  const Tile tile = find_tile(p, gridDim.x - 1 - blockIdx.x, group, kChunkRows<T, D>);
+  // Workgroups go to the 8 XCDs in turn: a KV head's tiles go to as few as can share them evenly, whose L2
+  // then holds that head's pages.  Later tiles see more keys: they begin first.
+  const int turn_of = blockIdx.x >> 3, xcd = blockIdx.x & 7, piece = blockIdx.y;
+  int head, slot;
+  if (8 % p.h_kv == 0) {
+    const int per = 8 / p.h_kv;
+    head = xcd / per;
+    slot = turn_of * per + xcd % per;
+  } else {
+    const int id = turn_of * 8 + xcd;
+    head = id / p.slots;
+    slot = id - head * p.slots;
+  }
+  if (slot >= p.slots || head >= p.h_kv) return;
+  const Tile tile = find_tile(p, p.slots - 1 - slot, group, kChunkRows);
   if (!tile.some) return;
   const int ns = pieces(p, tile);
   if (piece >= ns) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
 
-  int row_lo[NT], row_hi[NT];
-  bf16x8 q[NT][KS][NQ];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int row = tile.first + (wave * NT + t) * kRows + r;
+  int row_lo, row_hi;  // the keys that this lane's row sees
+  bf16x8 q[2 * KB][NQ];
+  {
+    const int row = tile.first + wave * 32 + c;
     const bool live = row < tile.rows;
     const int tok = row / group, hq = head * group + (row - tok * group);
     const int pos = tile.ctx - tile.len + tok;
-    row_hi[t] = live ? (p.causal ? min(tile.ctx, pos + 1) : tile.ctx) : 0;
-    row_lo[t] = live && p.window ? pos - p.window + 1 : 0;
+    row_hi = live ? (p.causal ? min(tile.ctx, pos + 1) : tile.ctx) : 0;
+    row_lo = live && p.window ? pos - p.window + 1 : 0;
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const int at = (k / 2) * 64 + g * 16 + (k & 1) * 8;
+    for (int k = 0; k < 2 * KB; ++k) {
+      const int at = (k / 2) * 32 + h * 16 + (k & 1) * 8;
       float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (live) load8(reinterpret_cast<const T*>(p.q) + (tile.begin + tok) * p.q_stride + (int64_t)hq * D + at, f);
       if constexpr (F32) {
-        split3_any(f, q[t][k]);
+        split3_any(f, q[k]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[t][k][0][i] = (__bf16)f[i];
+        for (int i = 0; i < 8; ++i) q[k][0][i] = (__bf16)f[i];
       }
     }
   }
-  f32x4 o[NT][MT];
-  float m[NT], l[NT];
+  f32x16 o[MT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    m[t] = -__builtin_inff();
-    l[t] = 0.f;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int i = 0; i < MT; ++i) o[i] = zeros16();
+  float m = -__builtin_inff(), l = 0.f;
 
   // what all of this wave's rows see, and what any of them does
-  int all_lo = 0, all_hi = INT32_MAX, any_lo = INT32_MAX, any_hi = 0;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const bool live = row_hi[t] > 0;
-    all_lo = max(all_lo, live ? row_lo[t] : 0);
-    all_hi = min(all_hi, live ? row_hi[t] : INT32_MAX);
-    any_lo = min(any_lo, live ? row_lo[t] : INT32_MAX);
-    any_hi = max(any_hi, row_hi[t]);
-  }
-  all_lo = wave_max(all_lo), all_hi = wave_min(all_hi), any_lo = wave_min(any_lo), any_hi = wave_max(any_hi);
+  const bool live_row = row_hi > 0;
+  const int all_lo = wave_max(live_row ? row_lo : 0), all_hi = wave_min(live_row ? row_hi : INT32_MAX);
+  const int any_lo = wave_min(live_row ? row_lo : INT32_MAX), any_hi = wave_max(row_hi);
 
   const int start = tile.lo + piece * p.piece;
   const int stop = min(tile.hi, start + p.piece);
@@ -536,7 +550,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendPara
   // this lane's part of the tile's copy: keys of the 16 tokens of group `wave`, values of the tokens of group vg
   const int vg = (lane & 3) ^ (lane >> 4);
   const int krow = lane / (D / 16);
-  const int k_from = krow * D + (((lane % (D / 16)) ^ (((krow & 3) | (wave << 2)) >> RS)) * 16);
+  const int k_from = krow * D + (((lane % (D / 16)) ^ (((krow & 7) | ((wave & 1) << 3)) >> RS)) * 16);
   const int v_from = ((lane >> 2) << p.page_shift) + (ONE ? 16 * vg : 0);
   auto stage = [&](int half, int k0, const Pages& t) {
     uint8_t* dst = tiles + half * kBytes + wave * (D * 16);
@@ -545,7 +559,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendPara
                         ((k0 + (ONE ? 0 : 16 * vg)) & in_page);
     auto copy = [&](auto J) {
       constexpr int j = decltype(J)::value;
-      to_lds<j * 1024>(ks + k_from, dst);
+      // (1024 bytes on, a key of 256 is 4 rows on: its place's exclusive-or changes by 4 pieces every other time)
+      to_lds<j * 1024>(ks + (D == 256 && (j & 1) ? k_from ^ 64 : k_from), dst);
       to_lds<0>(vs + v_from + ((16 * j) << p.page_shift), dst + kTok * D + j * 1024);
     };
     copy(std::integral_constant<int, 0>{});
@@ -553,8 +568,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendPara
     if constexpr (D > 128) copy(std::integral_constant<int, 2>{}), copy(std::integral_constant<int, 3>{});
   };
 
-  const int key_at = (16 * (r >> 2) + (r & 3)) * D + ((g ^ (r >> RS)) * 16);
-  const int value_at = kTok * D + r * 64 + ((g ^ (r >> 2)) * 16);
+  const int krow_c = 16 * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);  // this lane's row of the keys' operand: its token
+  const int key_at = krow_c * D + ((h ^ (((krow_c & 7) | ((krow_c >> 4) << 3)) >> RS)) * 16);
+  const int value_at = kTok * D + c * 64 + ((h ^ ((c >> 2) & 3)) * 16);
   // A tile that some row of the workgroup does not see whole: codes that must not reach the products are cleared
   // in LDS, those of tokens behind the context or of no page, and NaN (which the rows that see one get here).
   auto clear = [&](int half, int k0, const Pages& pages) {
@@ -565,26 +581,34 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendPara
       const int of = (i & 3) ^ ((i >> 4) & 3), id = Pages::of(pages.id, of);
       const int n = id >= 0 && id < p.pages ? tile.ctx - k0 - 16 * of : 0;
       uint4* at = reinterpret_cast<uint4*>(values + i * 16);
-      uint4 c = *at;
-      const uint2 a = first_codes(n), b = first_codes(n - 8);
-      c = make_uint4(c.x & a.x, c.y & a.y, c.z & b.x, c.w & b.y);
-      bad |= nan_bytes(c.x) | nan_bytes(c.y) | nan_bytes(c.z) | nan_bytes(c.w);
-      *at = c;
+      uint4 w = *at;
+      const uint2 x = first_codes(n), y = first_codes(n - 8);
+      w = make_uint4(w.x & x.x, w.y & x.y, w.z & y.x, w.w & y.y);
+      bad |= nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w);
+      *at = w;
     }
     if (!__syncthreads_or(bad != 0)) return;
-    const int ts = k0 + 16 * g;
+    // a product of ones (a code is NaN; 0x38 is e4m3's 1) and ones (the row sees the token)
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+      const int lo = row_lo - (k0 + 32 * u + 16 * h), hi = row_hi - (k0 + 32 * u + 16 * h);
+      float one[2][8];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+      for (int e = 0; e < 16; ++e) one[e >> 3][e & 7] = e >= lo && e < hi ? 1.f : 0.f;
+      typename P::vec see[2][P::N];
+      P::make(one[0], see[0]);
+      P::make(one[1], see[1]);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint2 c = *reinterpret_cast<const uint2*>(tiles + half * kBytes + value_at + i * 1024 + 8 * u);
-        const uint2 nan = make_uint2(nan_bytes(c.x), nan_bytes(c.y));
+      for (int i = 0; i < MT; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(tiles + half * kBytes + (value_at ^ (32 * u)) + i * 2048);
+        const uint4 nan = make_uint4(nan_bytes(w.x) * 0x38u, nan_bytes(w.y) * 0x38u, nan_bytes(w.z) * 0x38u, nan_bytes(w.w) * 0x38u);
+        f32x16 hit = mfma32(P::codes(nan.x, nan.y), see[0][0], zeros16());
+        hit = mfma32(P::codes(nan.z, nan.w), see[1][0], hit);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          give_nan<T>(nan, row_lo[t] - ts - 8 * u, row_hi[t] - ts - 8 * u, o[t][i]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int e = 0; e < 16; ++e) o[i][e] = hit[e] > 0.f ? __builtin_nanf("") : o[i][e];
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
     __syncthreads();
 #pragma unroll 1
     for (int i = threadIdx.x; i < 16 * D; i += kWaves * 64) {
@@ -596,107 +620,88 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendPara
 
   // whole: every row of the wave sees every token of the tile
   auto compute = [&](bool whole, int half, int k0, const Pages& pages) {
-    const int ts = k0 + 16 * g;
-    const int id = Pages::of(pages.id, g);
-    const bool held = id >= 0 && id < p.pages;
-    // (a scale of zero: scores of zero, and no 0 * infinity where they are masked)
-    const float unit = Pages::of(pages.ks, g) * p.scale_log2, f = held ? (unit == 0.f ? 1e-30f : unit) : 1.f;
-    const float vs = held ? Pages::of(pages.vs, g) : 1.f;
-    const float lv = fminf(fmaxf(__log2f(fabsf(vs)), -40.f), 120.f);
-    // Half a tile a turn (tokens 16 g + 8 u .. + 7 of every group): its scores are half the registers
+    // Half a tile a turn (tokens 32 u .. + 31): its scores are half the registers
 #pragma unroll 1
     for (int u = 0; u < 2; ++u) {
-      f32x4 s[NT][2];
+      const int ts = k0 + 32 * u + 16 * h;  // this lane's 16 tokens
+      const int id = Pages::of(pages.id, 2 * u + h);
+      const bool held = id >= 0 && id < p.pages;
+      // (a scale of zero: scores of zero, and no 0 * infinity where they are masked)
+      const float unit = Pages::of(pages.ks, 2 * u + h) * p.scale_log2, f = held ? (unit == 0.f ? 1e-30f : unit) : 1.f;
+      const float vs = held ? Pages::of(pages.vs, 2 * u + h) : 1.f;
+      const float lv = fminf(fmaxf(__log2f(fabsf(vs)), -40.f), 120.f);
+
+      f32x16 s = zeros16();
+      const int keys = half * kBytes + 32 * u * D + key_at;
+      auto key = [&](int b) { return *reinterpret_cast<const uint4*>(tiles + (keys ^ (b * 32))); };
+      uint4 w4[2] = {key(0), key(1)};
 #pragma unroll
-      for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int keys = half * kBytes + 8 * u * D + key_at;
-      auto key = [&](int b, int h) { return *reinterpret_cast<const uint4*>(tiles + (keys ^ (b * 64)) + 4 * h * D); };
-      uint4 c[2] = {key(0, 0), key(0, 1)};
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b) {
+      for (int b = 0; b < KB; b += 2) {
         uint4 next[2];
-        if (b + 1 < D / 64) next[0] = key(b + 1, 0), next[1] = key(b + 1, 1);
+        if (b + 2 < KB) next[0] = key(b + 2), next[1] = key(b + 3);
         __builtin_amdgcn_sched_barrier(0);  // asked for before this step's products, not where registers come free
 #pragma unroll
-        for (int i2 = 0; i2 < 4; ++i2) {
-          const int h = i2 & 1, hi = i2 >> 1;
-          const bf16x8 kk = hi ? to_bf16x8(c[h].z, c[h].w) : to_bf16x8(c[h].x, c[h].y);
+        for (int j = 0; j < 4; ++j) {
+          const uint4 w = w4[j >> 1];
+          const bf16x8 kk = j & 1 ? to_bf16x8(w.z, w.w) : to_bf16x8(w.x, w.y);
 #pragma unroll
-          for (int i = NQ - 1; i >= 0; --i)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) s[t][h] = mfma(kk, q[t][2 * b + hi][i], s[t][h]);
+          for (int i = NQ - 1; i >= 0; --i) s = mfma32(kk, q[2 * b + j][i], s);
         }
-        if (b + 1 < D / 64) c[0] = next[0], c[1] = next[1];
+        if (b + 2 < KB) w4[0] = next[0], w4[1] = next[1];
         __builtin_amdgcn_sched_barrier(0);
       }
       if (!whole) {
+        const int lo = row_lo - ts, hi = held ? row_hi - ts : 0;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int lo = row_lo[t] - ts - 8 * u, hi = held ? row_hi[t] - ts - 8 * u : 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < lo || e >= hi) s[t][e >> 2][e & 3] = -__builtin_inff();
-        }
+        for (int e = 0; e < 16; ++e)
+          if (e < lo || e >= hi) s[e] = -__builtin_inff();
       }
 
-      float top[NT];
-      bool grows = false;
+      float top = fmaxf(s[0], s[1]);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        top[t] = s[t][0][0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) top[t] = fmaxf(top[t], s[t][e >> 2][e & 3]);
-        top[t] = group_max(fmaf(top[t], f, lv));
-        grows = grows || top[t] > m[t] + 8.f;
-      }
+      for (int e = 2; e < 16; e += 2) top = max3(top, s[e], s[e + 1]);
+      top = half_max(fmaf(top, f, lv));
       // the maximum moves only where it grows by more than 2^8: the weights then stay under 256
-      if (__any(grows)) {
+      if (__any(top > m + 8.f)) {
+        const float now = fmaxf(m, top);
+        const float alpha = now == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - now);
+        m = now;
+        l *= alpha;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float now = fmaxf(m[t], top[t]);
-          const float alpha = now == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m[t] - now);
-          m[t] = now;
-          l[t] *= alpha;
-#pragma unroll
-          for (int i = 0; i < MT; ++i) o[t][i] *= alpha;
-        }
+        for (int i = 0; i < MT; ++i) o[i] *= alpha;
       }
-      typename P::vec pw[NT][P::N];
+      const float base = m == -__builtin_inff() ? 0.f : m;
+      typename P::vec pw[2][P::N];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
+      for (int j = 0; j < 2; ++j) {
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          w[e] = __builtin_amdgcn_exp2f(fmaf(s[t][e >> 2][e & 3], f, -base));
-          l[t] += w[e];
+          w[e] = __builtin_amdgcn_exp2f(fmaf(s[8 * j + e], f, -base));
+          l += w[e];
           w[e] *= vs;
         }
-        P::make(w, pw[t]);
+        P::make(w, pw[j]);
       }
 
-      const int values = half * kBytes + 8 * u + value_at;
-      auto value = [&](int i) { return *reinterpret_cast<const uint2*>(tiles + values + i * 1024); };
-      uint2 v[4] = {value(0), value(1), value(2), value(3)};
+      const int values = half * kBytes + (value_at ^ (32 * u));
+      auto value = [&](int i) { return *reinterpret_cast<const uint4*>(tiles + values + i * 2048); };
+      uint4 v[2] = {value(0), value(1)};
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < MT; i += 4) {
-        uint2 next[4];
-        if (i + 4 < MT)
-#pragma unroll
-          for (int h = 0; h < 4; ++h) next[h] = value(i + 4 + h);
+      for (int i = 0; i < MT; i += 2) {
+        uint4 next[2];
+        if (i + 2 < MT) next[0] = value(i + 2), next[1] = value(i + 3);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const typename P::vec vv = P::codes(v[h].x, v[h].y);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = P::N - 1; e >= 0; --e)
+          for (int x = 0; x < 2; ++x) {
+            const typename P::vec vv = j ? P::codes(v[x].z, v[x].w) : P::codes(v[x].x, v[x].y);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) o[t][i + h] = mfma(vv, pw[t][e], o[t][i + h]);
-        }
-        if (i + 4 < MT)
-#pragma unroll
-          for (int h = 0; h < 4; ++h) v[h] = next[h];
+            for (int e = P::N - 1; e >= 0; --e) o[i + x] = mfma32(vv, pw[j][e], o[i + x]);
+          }
+        if (i + 2 < MT) v[0] = next[0], v[1] = next[1];
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -730,28 +735,29 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_chunk_kernel(AttendPara
     half ^= 1;
   }
 
-  int row0 = tile.first + wave * (NT * kRows) + r;
-  asm volatile("" : "+v"(row0));  // worked out here, not kept through the loop
+  int row = tile.first + wave * 32 + c;
+  asm volatile("" : "+v"(row));  // what follows is worked out here, not kept through the loop
+  l += __shfl_xor(l, 32, 64);
+  if (row >= tile.rows) return;
+  const int64_t token = tile.begin + row / group;
+  const int hq = head * group + row % group;
+  const int64_t out = token * p.h_q + hq;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int row = row0 + t * kRows;
-    l[t] += __shfl_xor(l[t], 16, 64);
-    l[t] += __shfl_xor(l[t], 32, 64);
-    if (row >= tile.rows) continue;
-    const int64_t token = tile.begin + row / group;
-    const int h = head * group + row % group;
-    const int64_t out = token * p.h_q + h;
-    if (ns == 1) {
-      const float inv = l[t] == 0.f ? 0.f : 1.f / l[t];
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) put<T>(p, o[t][i] * inv, token, (int64_t)h * D + i * 16 + g * 4);
-      if (p.lse && g == 0) p.lse[out] = l[t] == 0.f ? -__builtin_inff() : (m[t] + __log2f(l[t])) * 0.69314718055994530942f;
-    } else {
-      const int64_t part = (int64_t)piece * p.tokens * p.h_q + out;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(p.part_o + part * D + i * 16 + g * 4) = o[t][i];
-      if (g == 0) p.part_ml[2 * part] = m[t], p.part_ml[2 * part + 1] = l[t];
+    for (int a = 0; a < 4; ++a) {
+      const int at = i * 32 + 8 * a + 4 * h;
+      const f32x4 y = f32x4{o[i][4 * a], o[i][4 * a + 1], o[i][4 * a + 2], o[i][4 * a + 3]};
+      if (ns == 1) put<T>(p, y * inv, token, (int64_t)hq * D + at);
+      else *reinterpret_cast<f32x4*>(p.part_o + ((int64_t)piece * p.tokens * p.h_q + out) * D + at) = y;
     }
+  if (h) return;
+  if (ns > 1) {
+    const int64_t part = (int64_t)piece * p.tokens * p.h_q + out;
+    p.part_ml[2 * part] = m, p.part_ml[2 * part + 1] = l;
+  } else if (p.lse) {
+    p.lse[out] = l == 0.f ? -__builtin_inff() : (m + __log2f(l)) * 0.69314718055994530942f;
   }
 }
 
@@ -818,7 +824,7 @@ Plan plan(const AttendShape& a) {
   c.uniform = a.tokens / a.n_seqs;
   // Sequences of 64 rows and more on average share their keys among a workgroup's waves.
   c.chunk = a.tokens * group >= (int64_t)a.n_seqs * 64;
-  c.tile_rows = !c.chunk ? kRows : chunk_rows(a.bf16, a.d);
+  c.tile_rows = !c.chunk ? kRows : kChunkRows;
   c.uniform_tiles = (int32_t)((c.uniform * group + c.tile_rows - 1) / c.tile_rows);
   c.slots = a.ragged ? a.tokens * group / c.tile_rows + a.n_seqs : (int64_t)c.uniform_tiles * a.n_seqs;
   // Pieces: about 4096 workgroups where the contexts allow it (16 for each CU: unequal contexts then even
@@ -838,8 +844,10 @@ Plan plan(const AttendShape& a) {
 template <typename T, int D>
 hipError_t launch(AttendParams p, const Plan& c, hipStream_t stream) {
   const dim3 grid((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)c.pieces);
-  if (c.chunk && p.page_shift >= 6) hipLaunchKernelGGL((attend_chunk_kernel<T, D, true>), grid, dim3(kWaves * 64), 0, stream, p);
-  else if (c.chunk) hipLaunchKernelGGL((attend_chunk_kernel<T, D, false>), grid, dim3(kWaves * 64), 0, stream, p);
+  const int64_t turns = (c.slots * p.h_kv + 7) / 8;
+  const dim3 chunks((unsigned)(turns * 8), (unsigned)c.pieces);
+  if (c.chunk && p.page_shift >= 6) hipLaunchKernelGGL((attend_chunk_kernel<T, D, true>), chunks, dim3(kWaves * 64), 0, stream, p);
+  else if (c.chunk) hipLaunchKernelGGL((attend_chunk_kernel<T, D, false>), chunks, dim3(kWaves * 64), 0, stream, p);
   else hipLaunchKernelGGL((attend_kernel<T, D>), grid, dim3(kWaves * 64), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || c.pieces == 1) return e;
@@ -876,6 +884,7 @@ hipError_t launch_attend(AttendParams p, const AttendShape& a, void* workspace, 
   p.uniform_tiles = c.uniform_tiles;
   p.piece = c.piece;
   p.tile_rows = c.tile_rows;
+  p.slots = (int32_t)c.slots;
   if (c.pieces > 1) {
     const size_t rows = (size_t)c.pieces * a.tokens * a.h_q;
     p.part_o = reinterpret_cast<float*>(workspace);

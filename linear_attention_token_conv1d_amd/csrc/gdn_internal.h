@@ -297,6 +297,7 @@ struct AttendParams {
   int64_t uniform;
   int32_t piece;
   int32_t tile_rows;
+  int32_t slots;
   float* part_o;   // [pieces, tokens, h_q, d]
   float* part_ml;  // [pieces, tokens, h_q, 2]
 };
