@@ -95,6 +95,12 @@ __device__ __forceinline__ float group_max(float v) {
   return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // The probabilities' operand and the values' type that goes with it.
 template <typename T> struct Probs;
 template <> struct Probs<__bf16> {
@@ -214,8 +220,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
   constexpr int NQ = F32 ? 3 : 1;
   constexpr int KS = D / 32, MT = D / 16;
   typedef Probs<T> P;
-  __shared__ float s_o[kWaves][kRows][D + 4];
+  // the queries' operands through the loop, then the waves' outputs
+  constexpr int kQBytes = KS * NQ * 64 * (int)sizeof(bf16x8), kOBytes = kWaves * kRows * (D + 4) * (int)sizeof(float);
+  __shared__ alignas(16) uint8_t lds[kQBytes > kOBytes ? kQBytes : kOBytes];
   __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
+  bf16x8* s_q = reinterpret_cast<bf16x8*>(lds);
+  float(*s_o)[kRows][D + 4] = reinterpret_cast<float(*)[kRows][D + 4]>(lds);
 
   const int group = p.h_q / p.h_kv;
   const int head = blockIdx.y, piece = blockIdx.z;
@@ -223,7 +233,41 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
   if (!tile.some) return;
   const int ns = pieces(p, tile);
   if (piece >= ns) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+
+  // A wave's codes stay on their way: a tile's keys are asked for when the last tile's have been used, and so
+  // are its values; its pages a tile before that.
+  const int start = tile.lo + piece * p.piece;
+  const int stop = min(tile.hi, start + p.piece);
+  const int32_t* table = p.page_table + (int64_t)tile.n * p.max_pages;
+  const int in_page = (1 << p.page_shift) - 1;
+  const int kg = r >> 2, ki = r & 3;  // this lane's row of the keys' operand: token 16 kg + 4 tt + ki
+  auto inside = [&](int id) { return id >= 0 && id < p.pages ? id : 0; };
+  // pages of this lane's 16 tokens as a row of the keys, and as a column of the scores
+  auto page_of = [&](int token) { return token < stop ? table[token >> p.page_shift] : -1; };
+  uint4 kc[4][D / 64], vc[MT];
+  auto load_keys = [&](int k0, int pk) {
+    const uint8_t* kp = p.k_cache + ((((int64_t)inside(pk) * p.h_kv + head) << p.page_shift) + ((k0 + 16 * kg) & in_page) + ki) * D + g * 16;
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) kc[tt][b] = *reinterpret_cast<const uint4*>(kp + tt * 4 * D + b * 64);
+  };
+  auto load_values = [&](int k0, int ps) {
+    const uint8_t* vp = p.v_cache + ((((int64_t)inside(ps) * p.h_kv + head) * D + r) << p.page_shift) + ((k0 + 16 * g) & in_page);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) vc[i] = *reinterpret_cast<const uint4*>(vp + ((i * 16) << p.page_shift));
+  };
+  constexpr int kStep = kWaves * kTok;
+  const int k_first = start + wave * kTok;
+  int pk = page_of(k_first + 16 * kg), ps = page_of(k_first + 16 * g);
+  int pk_next = page_of(k_first + kStep + 16 * kg), ps_next = page_of(k_first + kStep + 16 * g);
+  float ks = 0.f, vs = 0.f;
+  if (k_first < stop) {
+    load_keys(k_first, pk);
+    load_values(k_first, ps);
+    ks = p.k_scale[(int64_t)inside(ps) * p.h_kv + head], vs = p.v_scale[(int64_t)inside(ps) * p.h_kv + head];
+  }
 
   // this lane's row
   const int row = tile.first + r;
@@ -233,64 +277,59 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
   const int row_hi = live ? (p.causal ? min(tile.ctx, pos + 1) : tile.ctx) : 0;
   const int row_lo = p.window ? pos - p.window + 1 : 0;
 
-  // Q: lane (row r, group g) holds elements 64 b + 16 g .. + 15 of each 64, the order its keys come in
-  bf16x8 q[KS][NQ];
+  // Q: lane (row r, group g) holds elements 64 b + 16 g .. + 15 of each 64, the order its keys come in.  The
+  // four waves make the operands together.
 #pragma unroll
-  for (int k = 0; k < KS; ++k) {
+  for (int k = wave; k < KS; k += kWaves) {
     const int at = (k / 2) * 64 + g * 16 + (k & 1) * 8;
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (live) load8(reinterpret_cast<const T*>(p.q) + (tile.begin + tok) * p.q_stride + (int64_t)hq * D + at, f);
+    bf16x8 q[NQ];
     if constexpr (F32) {
-      split3_any(f, q[k]);
+      split3_any(f, q);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[k][0][i] = (__bf16)f[i];
+      for (int i = 0; i < 8; ++i) q[0][i] = (__bf16)f[i];
     }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) s_q[(k * NQ + i) * 64 + lane] = q[i];
   }
+  __syncthreads();
 
   f32x4 o[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -__builtin_inff(), l = 0.f;
 
-  const int start = tile.lo + piece * p.piece;
-  const int stop = min(tile.hi, start + p.piece);
-  const int32_t* table = p.page_table + (int64_t)tile.n * p.max_pages;
-  const int page = 1 << p.page_shift, in_page = page - 1;
-  const int kg = r >> 2, ki = r & 3;  // this lane's row of the keys' operand: token 16 kg + 4 tt + ki
-  for (int k0 = start + wave * kTok; k0 < stop; k0 += kWaves * kTok) {
-    // pages of this lane's 16 tokens as a row of the keys, and as a column of the scores
-    const int tk = k0 + 16 * kg, ts = k0 + 16 * g;
-    int pk = tk < stop ? table[tk >> p.page_shift] : -1;
-    int ps = ts < stop ? table[ts >> p.page_shift] : -1;
+#pragma unroll 1
+  for (int k0 = k_first; k0 < stop; k0 += kStep) {
+    const int ts = k0 + 16 * g;
     const bool held = ps >= 0 && ps < p.pages;  // a page outside the pool holds nothing
-    pk = pk >= 0 && pk < p.pages ? pk : 0;
-    ps = held ? ps : 0;
-    const float ks = p.k_scale[(int64_t)ps * p.h_kv + head], vs = p.v_scale[(int64_t)ps * p.h_kv + head];
-    const uint8_t* kp = p.k_cache + ((((int64_t)pk * p.h_kv + head) << p.page_shift) + (tk & in_page) + ki) * D + g * 16;
-    const uint8_t* vp = p.v_cache + ((((int64_t)ps * p.h_kv + head) * D) << p.page_shift) + (ts & in_page);
-    uint4 kc[4][D / 64], vc[MT];
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b) kc[tt][b] = *reinterpret_cast<const uint4*>(kp + tt * 4 * D + b * 64);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) vc[i] = *reinterpret_cast<const uint4*>(vp + ((i * 16 + r) << p.page_shift));
+    const bool more = k0 + kStep < stop;
+    float ks_next = 0.f, vs_next = 0.f;
+    if (more) ks_next = p.k_scale[(int64_t)inside(ps_next) * p.h_kv + head], vs_next = p.v_scale[(int64_t)inside(ps_next) * p.h_kv + head];
 
     f32x4 s[4];
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) s[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int b = 0; b < D / 64; ++b)
+    for (int b = 0; b < D / 64; ++b) {
+      bf16x8 q[2][NQ];
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) q[0][i] = s_q[(2 * b * NQ + i) * 64 + lane], q[1][i] = s_q[((2 * b + 1) * NQ + i) * 64 + lane];
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         const bf16x8 k_lo = to_bf16x8(kc[tt][b].x, kc[tt][b].y), k_hi = to_bf16x8(kc[tt][b].z, kc[tt][b].w);
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          s[tt] = mfma(k_lo, q[2 * b][NQ - 1 - i], s[tt]);
-          s[tt] = mfma(k_hi, q[2 * b + 1][NQ - 1 - i], s[tt]);
+        for (int i = NQ - 1; i >= 0; --i) {
+          s[tt] = mfma(k_lo, q[0][i], s[tt]);
+          s[tt] = mfma(k_hi, q[1][i], s[tt]);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (more) load_keys(k0 + kStep, pk_next);
+    __builtin_amdgcn_sched_barrier(0);
 
     // this lane's row against tokens ts .. ts + 15 (s[tt][i]: token ts + 4 tt + i): it sees from .. to - 1 of them
     const float f = ks * p.scale_log2;
@@ -302,18 +341,24 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
       for (int e = 0; e < 16; ++e)
         if (e < from || e >= to) s[e >> 2][e & 3] = -__builtin_inff();
     }
-    float top = -__builtin_inff();
+    float top = s[0][0];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) top = fmaxf(top, s[e >> 2][e & 3]);
+    for (int e = 1; e < 15; e += 2) top = max3(top, s[e >> 2][e & 3], s[(e + 1) >> 2][(e + 1) & 3]);
+    top = fmaxf(top, s[3][3]);
     // (the scales are positive, so the largest product is that of the largest score)
     top = sees ? fmaf(top, f, fminf(fmaxf(__log2f(fabsf(vs)), -40.f), 120.f)) : -__builtin_inff();
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float now = fmaxf(m, top);
-    const float base = now == -__builtin_inff() ? 0.f : now;
-    const float alpha = __builtin_amdgcn_exp2f(m - base);
-    m = now;
-    float w[2][8], sum = 0.f;
+    top = group_max(top);
+    // the maximum moves only where it grows by more than 2^8: the weights then stay under 256
+    if (__any(top > m + 8.f)) {
+      const float now = fmaxf(m, top);
+      const float alpha = now == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[i] *= alpha;
+    }
+    const float base = m == -__builtin_inff() ? 0.f : m;
+    float w[2][8];
 #pragma unroll
     for (int e = 0; e < 16; ++e) w[e >> 3][e & 7] = __builtin_amdgcn_exp2f(fmaf(s[e >> 2][e & 3], f, -base));
     if (part) {
@@ -324,10 +369,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
     const float factor = sees ? vs : 0.f;  // whatever stands where no page is
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      sum += w[e >> 3][e & 7];
+      l += w[e >> 3][e & 7];
       w[e >> 3][e & 7] *= factor;
     }
-    l = l * alpha + sum;
 
     if (part) {
       // codes that must not reach the product: tokens behind the context or of no page, and NaN
@@ -352,19 +396,23 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
     P::make(w[1], pw[1]);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      o[i] *= alpha;
       const typename P::vec v_lo = P::codes(vc[i].x, vc[i].y), v_hi = P::codes(vc[i].z, vc[i].w);
 #pragma unroll
-      for (int e = 0; e < P::N; ++e) {
-        o[i] = mfma(v_lo, pw[0][P::N - 1 - e], o[i]);
-        o[i] = mfma(v_hi, pw[1][P::N - 1 - e], o[i]);
+      for (int e = P::N - 1; e >= 0; --e) {
+        o[i] = mfma(v_lo, pw[0][e], o[i]);
+        o[i] = mfma(v_hi, pw[1][e], o[i]);
       }
+      if (i & 1) __builtin_amdgcn_sched_barrier(0);
     }
+    if (more) load_values(k0 + kStep, ps_next);
+    pk = pk_next, ps = ps_next, ks = ks_next, vs = vs_next;
+    pk_next = page_of(k0 + 2 * kStep + 16 * kg), ps_next = page_of(k0 + 2 * kStep + 16 * g);
   }
   l += __shfl_xor(l, 16, 64);
   l += __shfl_xor(l, 32, 64);
 
   // join the waves
+  __syncthreads();  // the queries have been read
   if (g == 0) s_m[wave][r] = m, s_l[wave][r] = l;
 #pragma unroll
   for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(&s_o[wave][r][i * 16 + g * 4]) = o[i];
@@ -419,11 +467,6 @@ __device__ __forceinline__ f32x16 zeros16() {
 #pragma unroll
   for (int i = 0; i < 16; ++i) z[i] = 0.f;
   return z;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
 }
 // The larger of lanes l and l ^ 32.
 __device__ __forceinline__ float half_max(float v) {
@@ -761,44 +804,54 @@ __global__ __launch_bounds__(kWaves * 64, sizeof(T) == 4 && D == 256 ? 1 : 2) vo
   }
 }
 
-// Joins the pieces of a row: a wave a row, its lanes over the head's elements.
+// Joins the pieces of a row: a wave a row, its lanes over the head's elements.  Lane s works out the factor of
+// piece s, and the pieces' rows are read several at a time.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_kernel(AttendParams p) {
   const int group = p.h_q / p.h_kv, lane = threadIdx.x & 63;
   const Tile tile = find_tile(p, blockIdx.x, group, p.tile_rows);
   if (!tile.some) return;
   const int ns = pieces(p, tile);
-  if (ns == 1) return;  // written already
-  for (int rr = threadIdx.x >> 6; rr < p.tile_rows; rr += 4) {
-    const int at = tile.first + rr;
-    if (at >= tile.rows) return;
-    const int64_t token = tile.begin + at / group;
-    const int h = blockIdx.y * group + at % group;
-    const int64_t out = token * p.h_q + h, step = p.tokens * p.h_q;
-    float mm = -__builtin_inff();
-    for (int s = 0; s < ns; ++s) mm = fmaxf(mm, p.part_ml[2 * (s * step + out)]);
-    const float base = mm == -__builtin_inff() ? 0.f : mm;
-    constexpr int E = D / 64;
-    float sum[E], ll = 0.f;
+  const int at = tile.first + blockIdx.z * 4 + (threadIdx.x >> 6);
+  if (ns == 1 || at >= tile.rows) return;  // written already, or no row
+  const int64_t token = tile.begin + at / group;
+  const int h = blockIdx.y * group + at % group;
+  const int64_t out = token * p.h_q + h, step = p.tokens * p.h_q;
+  float mm = -__builtin_inff();
+  for (int s = lane; s < ns; s += 64) mm = fmaxf(mm, p.part_ml[2 * (s * step + out)]);
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] = 0.f;
-    for (int s = 0; s < ns; ++s) {
-      const int64_t part = s * step + out;
-      const float a = __builtin_amdgcn_exp2f(p.part_ml[2 * part] - base);
+  for (int x = 32; x >= 1; x >>= 1) mm = fmaxf(mm, __shfl_xor(mm, x, 64));
+  const float base = mm == -__builtin_inff() ? 0.f : mm;
+  constexpr int E = D / 64;
+  float sum[E], ll = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[e] = 0.f;
+  for (int s0 = 0; s0 < ns; s0 += 64) {
+    float a = 0.f;
+    if (s0 + lane < ns) {
+      const int64_t part = (s0 + lane) * step + out;
+      a = __builtin_amdgcn_exp2f(p.part_ml[2 * part] - base);
       ll += a * p.part_ml[2 * part + 1];
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum[e] += a * p.part_o[part * D + e * 64 + lane];
     }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int n = min(64, ns - s0);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float as = __shfl(a, s, 64);
+      const float* row = p.part_o + ((s0 + s) * step + out) * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int64_t c = (int64_t)h * D + e * 64 + lane;
-      float y = sum[e] * inv;
-      if (p.gate) y = gated<T>(y, to_f32(reinterpret_cast<const T*>(p.gate)[token * p.gate_stride + c]));
-      reinterpret_cast<T*>(p.o)[token * p.o_stride + c] = from_f32<T>(y);
+      for (int e = 0; e < E; ++e) sum[e] = fmaf(as, row[e], sum[e]);
     }
-    if (p.lse && lane == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (mm + __log2f(ll)) * 0.69314718055994530942f;
   }
+  ll = wave_sum(ll);
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;
+  const int64_t c = (int64_t)h * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    float y = sum[e] * inv;
+    if (p.gate) y = gated<T>(y, to_f32(reinterpret_cast<const T*>(p.gate)[token * p.gate_stride + c + e]));
+    reinterpret_cast<T*>(p.o)[token * p.o_stride + c + e] = from_f32<T>(y);
+  }
+  if (p.lse && lane == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (mm + __log2f(ll)) * 0.69314718055994530942f;
 }
 
 // How a call is cut: tiles of rows, and pieces of the context of `piece` tokens.
@@ -834,7 +887,7 @@ Plan plan(const AttendShape& a) {
   int64_t piece = most;
   if (!c.chunk || tiles < 512) piece = (int64_t)std::min((double)most, (double)most * tiles / (c.chunk ? 1024 : 4096));
   piece = (piece + step - 1) / step * step;
-  if (c.chunk) if (const char* e = getenv("XPIECE")) piece = atoi(e);
+  if (const char* e = getenv(c.chunk ? "XPIECE" : "XPIECED")) piece = atoi(e);
   c.piece = (int32_t)(piece < step ? step : piece);
   c.pieces = (most + c.piece - 1) / c.piece;
   if (c.pieces < 1) c.pieces = 1;
@@ -851,7 +904,8 @@ hipError_t launch(AttendParams p, const Plan& c, hipStream_t stream) {
   else hipLaunchKernelGGL((attend_kernel<T, D>), grid, dim3(kWaves * 64), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || c.pieces == 1) return e;
-  hipLaunchKernelGGL((join_kernel<T, D>), dim3((unsigned)c.slots, (unsigned)p.h_kv), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL((join_kernel<T, D>), dim3((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)(c.tile_rows / 4)), dim3(256), 0,
+                     stream, p);
   return hipGetLastError();
 }
 
