@@ -221,7 +221,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
   constexpr int KS = D / 32, MT = D / 16;
   typedef Probs<T> P;
   // the queries' operands through the loop, then the waves' outputs
-  constexpr int kQBytes = KS * NQ * 64 * (int)sizeof(bf16x8), kOBytes = kWaves * kRows * (D + 4) * (int)sizeof(float);
+  constexpr int kQBytes = KS * NQ * 64 * (int)sizeof(bf16x8), kOBytes = 2 * kRows * (D + 4) * (int)sizeof(float);
   __shared__ alignas(16) uint8_t lds[kQBytes > kOBytes ? kQBytes : kOBytes];
   __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
   bf16x8* s_q = reinterpret_cast<bf16x8*>(lds);
@@ -229,7 +229,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
 
   const int group = p.h_q / p.h_kv;
   const int head = blockIdx.y, piece = blockIdx.z;
-  const Tile tile = find_tile(p, blockIdx.x, group, kRows);
+  // workgroups go to the 8 XCDs in turn: every XCD gets pieces of every sequence, however unequal those are
+  const Tile tile = find_tile(p, (blockIdx.x + piece) % gridDim.x, group, kRows);
   if (!tile.some) return;
   const int ns = pieces(p, tile);
   if (piece >= ns) return;
@@ -411,38 +412,49 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
   l += __shfl_xor(l, 16, 64);
   l += __shfl_xor(l, 32, 64);
 
-  // join the waves
+  // Join the waves by their maxima and sums; rows pass through LDS two waves' at a time, so that two workgroups'
+  // fit a CU with room to spare.
   __syncthreads();  // the queries have been read
-  if (g == 0) s_m[wave][r] = m, s_l[wave][r] = l;
-#pragma unroll
-  for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(&s_o[wave][r][i * 16 + g * 4]) = o[i];
+  if (g == 0) s_m[wave][r] = m;
   __syncthreads();
+  float mm = s_m[0][r];
+#pragma unroll
+  for (int k = 1; k < kWaves; ++k) mm = fmaxf(mm, s_m[k][r]);
+  const float a = mm == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - mm);
+  if (g == 0) s_l[wave][r] = a * l;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) o[i] *= a;
+#pragma unroll
+  for (int turn = 0; turn < 2; ++turn) {
+    if (live && (turn ? wave < 2 : wave >= 2)) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        f32x4* at = reinterpret_cast<f32x4*>(&s_o[wave & 1][r][i * 16 + g * 4]);
+        *at = turn ? *at + o[i] : o[i];
+      }
+    }
+    __syncthreads();
+  }
   for (int i = threadIdx.x; i < kRows * D / 4; i += kWaves * 64) {
     const int rr = i / (D / 4), c = (i - rr * (D / 4)) * 4, at = tile.first + rr;
     if (at >= tile.rows) break;
-    float mm = s_m[0][rr];
+    float top = s_m[0][rr], ll = 0.f;
 #pragma unroll
-    for (int k = 1; k < kWaves; ++k) mm = fmaxf(mm, s_m[k][rr]);
-    const float base = mm == -__builtin_inff() ? 0.f : mm;
-    f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
-    float ll = 0.f;
+    for (int k = 1; k < kWaves; ++k) top = fmaxf(top, s_m[k][rr]);
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) {
-      const float a = __builtin_amdgcn_exp2f(s_m[k][rr] - base);
-      ll += a * s_l[k][rr];
-      sum += a * *reinterpret_cast<const f32x4*>(&s_o[k][rr][c]);
-    }
+    for (int k = 0; k < kWaves; ++k) ll += s_l[k][rr];
+    const f32x4 sum = *reinterpret_cast<const f32x4*>(&s_o[0][rr][c]) + *reinterpret_cast<const f32x4*>(&s_o[1][rr][c]);
     const int64_t token = tile.begin + at / group;
     const int h = head * group + at % group;
     const int64_t out = token * p.h_q + h;
     if (ns == 1) {
       const float inv = ll == 0.f ? 0.f : 1.f / ll;
       put<T>(p, sum * inv, token, (int64_t)h * D + c);
-      if (p.lse && c == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (mm + __log2f(ll)) * 0.69314718055994530942f;
+      if (p.lse && c == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (top + __log2f(ll)) * 0.69314718055994530942f;
     } else {
       const int64_t part = (int64_t)piece * p.tokens * p.h_q + out;
       *reinterpret_cast<f32x4*>(p.part_o + part * D + c) = sum;
-      if (c == 0) p.part_ml[2 * part] = mm, p.part_ml[2 * part + 1] = ll;
+      if (c == 0) p.part_ml[2 * part] = top, p.part_ml[2 * part + 1] = ll;
     }
   }
 }
