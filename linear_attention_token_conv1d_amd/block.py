@@ -120,15 +120,17 @@ def _rows(t, name, index, shape, dtype):
         return None, 0
     if not isinstance(t, torch.Tensor) or t.get_device() != index:
         raise GdnError(f"{name} must be on the same GPU as the call's other tensors")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise GdnError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise GdnError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1] if len(shape) == 2 else shape[1] * shape[2]
     s = t.stride()
-    # a stride over one element, or none at all, says nothing about the layout
+    # a stride over one element says nothing about the layout
     if (s[-1] != 1 and shape[-1] > 1) or (len(s) == 3 and s[1] != shape[2] and shape[1] > 1):
         raise GdnError(f"{name} must have contiguous heads inside a token")
-    return t.data_ptr(), (s[0] if shape[0] > 1 else t[0].numel() if shape[0] else 0)
+    return t.data_ptr(), s[0]
 
 
 def _norm_shape(x):
@@ -165,10 +167,10 @@ def rms_norm(x, weight=None, gate=None, residual=None, order="pre", activation="
     index, shape, heads, width = _norm_shape(x)
     order, act = _norm_how(weight, gate, order, activation)
     dt = x.dtype
-    y = torch.empty(shape, dtype=dt, device=x.device) if out is None else out
+    y = torch.empty_like(x) if out is None else out
     sums = residual is not None and order == 0
     if sums and sum_out is None:
-        sum_out = torch.empty(shape, dtype=dt, device=x.device)
+        sum_out = torch.empty_like(residual)
     if not sums and sum_out is not None:
         raise GdnError("sum_out goes with a residual in the pre order")
     px, sx = _rows(x, "x", index, shape, dt)
@@ -201,12 +203,12 @@ def rms_norm_backward(x, dy, weight=None, gate=None, d_sum=None, residual=False,
         raise GdnError("residual and d_sum belong to the pre order: in the post order the residual's gradient is dy")
     if order == 0 and not residual and scale != 1.0:
         raise GdnError("the pre order scales x only where it is added to a residual")
-    dx = torch.empty(shape, dtype=dt, device=dev) if dx is None else dx
+    dx = torch.empty_like(x) if dx is None else dx
     dres = None
     if residual:
-        dres = dx if scale == 1.0 else torch.empty(shape, dtype=dt, device=dev)
+        dres = dx if scale == 1.0 else torch.empty_like(x)
     if gate is not None and dgate is None:
-        dgate = torch.empty(shape, dtype=dt, device=dev)
+        dgate = torch.empty_like(gate)
     px, sx = _rows(x, "x", index, shape, dt)
     pg, sg = _rows(gate, "gate", index, shape, dt)
     pd, sd = _rows(dy, "dy", index, shape, dt)
@@ -296,7 +298,7 @@ def _rope(q, positions, inv_freq, k, layout, mscale, inverse, out, k_out):
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
         raise GdnError("inv_freq must be a [rot / 2] tensor")
     pf = _tensor(inv_freq, "inv_freq", index, inv_freq.shape, torch.float64)
-    y = torch.empty(q.shape, dtype=dt, device=q.device) if out is None else out
+    y = torch.empty_like(q) if out is None else out
     py, sy = _rows(y, "out", index, q.shape, dt)
     h_k, pk, sk, pz, sz, z = 0, None, 0, None, 0, None
     if k is not None:
@@ -304,7 +306,7 @@ def _rope(q, positions, inv_freq, k, layout, mscale, inverse, out, k_out):
         if k.shape[0] != T or k.shape[2] != d:
             raise GdnError(f"k must be [{T}, H, {d}], got {list(k.shape)}")
         h_k = k.shape[1]
-        z = torch.empty(k.shape, dtype=dt, device=q.device) if k_out is None else k_out
+        z = torch.empty_like(k) if k_out is None else k_out
         pz, sz = _rows(z, "k_out", index, k.shape, dt)
     elif k_out is not None:
         raise GdnError("k_out goes with k")
@@ -420,7 +422,7 @@ def cache_attention(q, cache, page_table, lens, cu_seqlens=None, scale=None, cau
     pages, page, pkc, pvc, pks, pvs = _cache(cache, index, h, d)
     n, width, pt, pl, pc = _sequences(page_table, lens, cu_seqlens, index, T)
     pg, sg = _rows(gate, "gate", index, q.shape, dt)
-    o = torch.empty(q.shape, dtype=dt, device=q.device) if out is None else out
+    o = torch.empty_like(q) if out is None else out
     po, so = _rows(o, "out", index, q.shape, dt)
     lse = torch.empty((T, h_q), dtype=torch.float32, device=q.device) if return_lse else None
     a = CacheAttentionArgs(ctypes.sizeof(CacheAttentionArgs), _DT[dt], n, h_q, h, d, page, pages, width, 1 if causal else 0, window,

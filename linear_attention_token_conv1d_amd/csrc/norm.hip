@@ -32,7 +32,7 @@ namespace {
 constexpr int kThreads = 256;
 
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
+struct alignas(sizeof(T) * VEC > 16 ? 16 : sizeof(T) * VEC) Pack {
   T v[VEC];
 };
 template <typename T, int VEC>
@@ -47,16 +47,22 @@ __device__ __forceinline__ void store_pack(void* base, int64_t at, const float (
   *reinterpret_cast<Pack<T, VEC>*>(reinterpret_cast<T*>(base) + at) = p;
 }
 
-// weights are in the io dtype or in fp32 (gdn_rms_norm_args.weight_dtype)
+// Weights are bf16 or fp32 whatever the rows are; without any they are ones.
 template <int VEC>
-__device__ __forceinline__ void load_weight(const void* w, int bf16, int at, float offset, float (&f)[VEC]) {
+struct Weight {
+  Pack<float, VEC> v;  // fp32 as it is, bf16 in its first half
+  __device__ __forceinline__ void load(const void* w, int bf16, int at) {
+    if (!w) return;
+    if (bf16) {
+      const Pack<__bf16, VEC> h = load_pack<__bf16, VEC>(w, at);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    f[e] = w ? offset + (bf16 ? to_f32(reinterpret_cast<const __bf16*>(w)[at + e])
-                              : reinterpret_cast<const float*>(w)[at + e])
-             : 1.0f;
+      for (int e = 0; e < VEC; ++e) v.v[e] = to_f32(h.v[e]);
+    } else {
+      v = load_pack<float, VEC>(w, at);
+    }
   }
-}
+  __device__ __forceinline__ float get(const void* w, float offset, int e) const { return w ? offset + v.v[e] : 1.0f; }
+};
 
 // Sigmoid: the hardware exponential for bf16 rows; for fp32 rows expf, whose
 // error stays at an ulp for large arguments.
@@ -95,6 +101,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
   const bool sum = p.order == 0 && p.residual;
 
   Pack<T, VEC> x[NV], res[NV], z[NV];
+  Weight<VEC> w[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int at = (v * G + lane) * VEC;
@@ -102,6 +109,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
     x[v] = load_pack<T, VEC>(p.x, t * p.x_stride + col + at);
     if (p.residual) res[v] = load_pack<T, VEC>(p.residual, t * p.residual_stride + col + at);
     if (p.gate) z[v] = load_pack<T, VEC>(p.gate, t * p.gate_stride + col + at);
+    w[v].load(p.weight, p.weight_bf16, at);
   }
   float h[NV][VEC], ss[1] = {0.f};
 #pragma unroll
@@ -121,11 +129,10 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
   for (int v = 0; v < NV; ++v) {
     const int at = (v * G + lane) * VEC;
     if (at >= p.width) continue;
-    float w[VEC], y[VEC];
-    load_weight<VEC>(p.weight, p.weight_bf16, at, p.weight_offset, w);
+    float y[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      y[e] = h[v][e] * r * w[e];
+      y[e] = h[v][e] * r * w[v].get(p.weight, p.weight_offset, e);
       if (p.gate) {
         const float zz = to_f32(z[v].v[e]), s = sigmoid<T>(zz);
         y[e] *= p.act == 1 ? zz * s : s;
@@ -142,80 +149,115 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p
   constexpr int kGroups = kThreads / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
   float dw[NV][VEC];
+  Weight<VEC> w[NV];
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < NV; ++v) {
+    const int at = (v * G + lane) * VEC;
+    if (at < p.width) w[v].load(p.weight, p.weight_bf16, at);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[v][e] = 0.f;
+  }
 
-  // every group of a workgroup makes the same number of turns
-  for (int64_t first = (int64_t)blockIdx.x * kGroups; first < p.rows; first += (int64_t)gridDim.x * kGroups) {
-    const bool live = first + group < p.rows;
-    const uint32_t row = (uint32_t)(live ? first + group : p.rows - 1);
-    const uint32_t t = row / (uint32_t)p.heads;
-    const int64_t col = (int64_t)(row - t * (uint32_t)p.heads) * p.width;
+  struct Row {
     Pack<T, VEC> x[NV], g[NV], z[NV], ds[NV];
+  };
+  // every group of a workgroup makes the same number of turns; one beyond the last row follows along on that row
+  auto at_row = [&](int64_t row, uint32_t& t, int64_t& col) {
+    const uint32_t r = (uint32_t)(row < p.rows ? row : p.rows - 1);
+    t = r / (uint32_t)p.heads;
+    col = (int64_t)(r - t * (uint32_t)p.heads) * p.width;
+  };
+  auto load = [&](Row& d, int64_t row) {
+    uint32_t t;
+    int64_t col;
+    at_row(row, t, col);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int at = (v * G + lane) * VEC;
       if (at >= p.width) continue;
-      x[v] = load_pack<T, VEC>(p.x, t * p.x_stride + col + at);
-      g[v] = load_pack<T, VEC>(p.dy, t * p.dy_stride + col + at);
-      if (p.gate) z[v] = load_pack<T, VEC>(p.gate, t * p.gate_stride + col + at);
-      if (p.d_sum) ds[v] = load_pack<T, VEC>(p.d_sum, t * p.d_sum_stride + col + at);
+      d.x[v] = load_pack<T, VEC>(p.x, t * p.x_stride + col + at);
+      d.g[v] = load_pack<T, VEC>(p.dy, t * p.dy_stride + col + at);
+      if (p.gate) d.z[v] = load_pack<T, VEC>(p.gate, t * p.gate_stride + col + at);
+      if (p.d_sum) d.ds[v] = load_pack<T, VEC>(p.d_sum, t * p.d_sum_stride + col + at);
     }
+  };
+  const float post = p.order == 1 ? p.scale : 1.0f, inv_width = 1.0f / (float)p.width;
+  auto work = [&](const Row& d, int64_t row) {
     float sums[2] = {0.f, 0.f};  // of h^2 and of u h
+    float s[NV][VEC];            // sigmoid of the gate
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int at = (v * G + lane) * VEC;
-      if (at >= p.width) continue;
-      float w[VEC];
-      load_weight<VEC>(p.weight, p.weight_bf16, at, p.weight_offset, w);
+      if ((v * G + lane) * VEC >= p.width) continue;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float h = to_f32(x[v].v[e]);
-        float u = to_f32(g[v].v[e]) * w[e];
+        const float h = to_f32(d.x[v].v[e]);
+        float u = to_f32(d.g[v].v[e]) * w[v].get(p.weight, p.weight_offset, e);
         if (p.gate) {
-          const float zz = to_f32(z[v].v[e]), s = sigmoid<T>(zz);
-          u *= p.act == 1 ? zz * s : s;
+          const float z = to_f32(d.z[v].v[e]);
+          s[v][e] = sigmoid<T>(z);
+          u *= p.act == 1 ? z * s[v][e] : s[v][e];
         }
         sums[0] = fmaf(h, h, sums[0]);
         sums[1] = fmaf(u, h, sums[1]);
       }
     }
     group_sum<G>(sums);
-    const float r = 1.0f / sqrtf(sums[0] / (float)p.width + p.eps);
-    const float post = p.order == 1 ? p.scale : 1.0f;
-    const float c = r * r * sums[1] / (float)p.width;  // r mean(u n) = r^2 mean(u h)
-    if (live) {
+    const float r = 1.0f / sqrtf(sums[0] * inv_width + p.eps);
+    const float c = post * r * r * r * (sums[1] * inv_width);  // dh = r u - c h:  r mean(u n) n = r^3 mean(u h) h
+    if (row >= p.rows) return;
+    uint32_t t;
+    int64_t col;
+    at_row(row, t, col);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int at = (v * G + lane) * VEC;
-        if (at >= p.width) continue;
-        float w[VEC], dx[VEC], dz[VEC];
-        load_weight<VEC>(p.weight, p.weight_bf16, at, p.weight_offset, w);
+    for (int v = 0; v < NV; ++v) {
+      const int at = (v * G + lane) * VEC;
+      if (at >= p.width) continue;
+      float dx[VEC], dz[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float n = to_f32(x[v].v[e]) * r, dy = post * to_f32(g[v].v[e]);
-          float a = 1.f, slope = 0.f;
-          if (p.gate) {
-            const float zz = to_f32(z[v].v[e]), s = sigmoid<T>(zz);
-            a = p.act == 1 ? zz * s : s;
-            slope = p.act == 1 ? s * (1.f + zz * (1.f - s)) : s * (1.f - s);
-          }
-          dx[e] = r * (dy * w[e] * a) - n * (post * c);
-          if (p.d_sum) dx[e] += to_f32(ds[v].v[e]);
-          dz[e] = dy * n * w[e] * slope;
-          dw[v][e] = fmaf(dy * n, a, dw[v][e]);
+      for (int e = 0; e < VEC; ++e) {
+        const float h = to_f32(d.x[v].v[e]), dyr = post * r * to_f32(d.g[v].v[e]), wt = w[v].get(p.weight, p.weight_offset, e);
+        float a = 1.f;
+        const float nd = dyr * h;  // dy n
+        if (p.gate) {
+          const float z = to_f32(d.z[v].v[e]), sg = s[v][e];
+          a = p.act == 1 ? z * sg : sg;
+          dz[e] = nd * wt * (p.act == 1 ? sg * (1.f + z * (1.f - sg)) : sg * (1.f - sg));
         }
-        if (p.d_residual) store_pack<T, VEC>(p.d_residual, t * p.d_residual_stride + col + at, dx);
-        if (p.dx) {
-          if (p.order == 0)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) dx[e] *= p.scale;
-          store_pack<T, VEC>(p.dx, t * p.dx_stride + col + at, dx);
-        }
-        if (p.gate) store_pack<T, VEC>(p.dgate, t * p.dgate_stride + col + at, dz);
+        dx[e] = fmaf(-c, h, dyr * wt * a);
+        if (p.d_sum) dx[e] += to_f32(d.ds[v].v[e]);
+        dw[v][e] = fmaf(nd, a, dw[v][e]);
       }
+      if (p.d_residual) store_pack<T, VEC>(p.d_residual, t * p.d_residual_stride + col + at, dx);
+      if (p.dx) {
+        if (p.order == 0)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) dx[e] *= p.scale;
+        store_pack<T, VEC>(p.dx, t * p.dx_stride + col + at, dx);
+      }
+      if (p.gate) store_pack<T, VEC>(p.dgate, t * p.dgate_stride + col + at, dz);
+    }
+  };
+
+  const int64_t step = (int64_t)gridDim.x * kGroups;
+  const int64_t begin = (int64_t)blockIdx.x * kGroups;
+  if constexpr (NV * VEC <= 24) {
+    // the next row is on its way while one is worked on (it is no row's output: p.dx and the others may be an
+    // input's own rows, but each row is read by the group that writes it)
+    Row a, b;
+    if (begin < p.rows) load(a, begin + group);
+    for (int64_t first = begin; first < p.rows; first += 2 * step) {
+      const bool second = first + step < p.rows;
+      if (second) load(b, first + step + group);
+      work(a, first + group);
+      if (!second) break;
+      if (first + 2 * step < p.rows) load(a, first + 2 * step + group);
+      work(b, first + step + group);
+    }
+  } else {
+    for (int64_t first = begin; first < p.rows; first += step) {
+      Row a;
+      load(a, first + group);
+      work(a, first + group);
     }
   }
   if (!partial) return;
@@ -243,19 +285,30 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p
   }
 }
 
-// dw[c] = sum of the partial rows: 32 columns a workgroup, 32 row lanes whose
+// dw[c] = sum of the partial rows: 16 columns a workgroup, 64 row lanes, four rows of each at a time; the lanes'
 // sums join in LDS in a fixed order.
 __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* partial, int blocks, int width, float* dw) {
-  __shared__ float s[32][33];
-  const int c = threadIdx.x & 31, k = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
-  float a = 0.f;
+  __shared__ float s[64][17];
+  const int c = threadIdx.x & 15, k = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
   if (col < width)
-    for (int b = k; b < blocks; b += 32) a += partial[(int64_t)b * width + col];
-  s[k][c] = a;
+    for (int b = k; b < blocks; b += 256)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (b + 64 * i < blocks) a[i] += partial[(int64_t)(b + 64 * i) * width + col];
+  s[k][c] = (a[0] + a[1]) + (a[2] + a[3]);
+  __syncthreads();
+  if (k < 8) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += s[k * 8 + i][c];
+    s[k * 8][c] = t;
+  }
   __syncthreads();
   if (k == 0 && col < width) {
     float t = 0.f;
-    for (int i = 0; i < 32; ++i) t += s[i][c];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += s[i * 8][c];
     dw[col] = t;
   }
 }
@@ -297,9 +350,9 @@ hipError_t dispatch(int width, bool vec, F&& f) {
 
 // The most workgroups of the backward: enough to fill the chip, few enough
 // that their partial dw rows stay small beside the rows themselves.
-int backward_blocks(int64_t rows, int width) {
-  const int64_t most = width <= 1024 ? 2048 : 1024;
-  return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
+constexpr int kMostBlocks = 1024;
+int backward_blocks(int64_t rows) {
+  return (int)(rows < kMostBlocks ? (rows > 0 ? rows : 1) : kMostBlocks);
 }
 
 template <typename T>
@@ -333,7 +386,7 @@ template <typename T>
 hipError_t forward(const NormParams& p, hipStream_t stream) {
   constexpr int V = 16 / (int)sizeof(T);
   const size_t es = sizeof(T);
-  const bool vec = p.width % V == 0 && vec_ok(p.x, p.x_stride, V, es) && vec_ok(p.gate, p.gate_stride, V, es) &&
+  const bool vec = p.width % V == 0 && vec_ok(p.weight, 0, V, p.weight_bf16 ? 2 : 4) && vec_ok(p.x, p.x_stride, V, es) && vec_ok(p.gate, p.gate_stride, V, es) &&
                    vec_ok(p.residual, p.residual_stride, V, es) && vec_ok(p.y, p.y_stride, V, es) &&
                    vec_ok(p.sum, p.sum_stride, V, es);
   return dispatch<T>(p.width, vec, Forward<T>{p, stream});
@@ -342,7 +395,7 @@ template <typename T>
 hipError_t backward(const NormBwdParams& p, hipStream_t stream, int* blocks) {
   constexpr int V = 16 / (int)sizeof(T);
   const size_t es = sizeof(T);
-  const bool vec = p.width % V == 0 && vec_ok(p.x, p.x_stride, V, es) && vec_ok(p.gate, p.gate_stride, V, es) &&
+  const bool vec = p.width % V == 0 && vec_ok(p.weight, 0, V, p.weight_bf16 ? 2 : 4) && vec_ok(p.x, p.x_stride, V, es) && vec_ok(p.gate, p.gate_stride, V, es) &&
                    vec_ok(p.dy, p.dy_stride, V, es) && vec_ok(p.d_sum, p.d_sum_stride, V, es) &&
                    vec_ok(p.dx, p.dx_stride, V, es) && vec_ok(p.dgate, p.dgate_stride, V, es) &&
                    vec_ok(p.d_residual, p.d_residual_stride, V, es);
@@ -352,7 +405,7 @@ hipError_t backward(const NormBwdParams& p, hipStream_t stream, int* blocks) {
 }  // namespace
 
 size_t norm_backward_workspace_bytes(int64_t rows, int width) {
-  return (size_t)backward_blocks(rows, width) * width * sizeof(float);
+  return (size_t)backward_blocks(rows) * width * sizeof(float);
 }
 
 hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t stream) {
@@ -363,12 +416,12 @@ hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t stream) {
 hipError_t launch_norm_backward(const NormBwdParams& p, int dtype, hipStream_t stream) {
   int blocks = 0;  // no rows: dw is the sum of nothing
   if (p.rows > 0) {
-    blocks = backward_blocks(p.rows, p.width);
+    blocks = backward_blocks(p.rows);
     const hipError_t e = dtype == 1 ? backward<__bf16>(p, stream, &blocks) : backward<float>(p, stream, &blocks);
     if (e != hipSuccess) return e;
   }
   if (!p.dweight) return hipSuccess;
-  hipLaunchKernelGGL(norm_dweight_kernel, dim3((unsigned)((p.width + 31) / 32)), dim3(1024), 0, stream,
+  hipLaunchKernelGGL(norm_dweight_kernel, dim3((unsigned)((p.width + 15) / 16)), dim3(1024), 0, stream,
                      reinterpret_cast<const float*>(p.workspace), blocks, p.width, p.dweight);
   return hipGetLastError();
 }
