@@ -71,9 +71,86 @@ __device__ __forceinline__ void find_slot(const CacheStoreParams& p, int slot, i
   j = slot - (cu[lo] / p.page + 2 * lo);
 }
 
-template <typename T, int THREADS>
-__global__ __launch_bounds__(THREADS) void cache_store_kernel(CacheStoreParams p) {
-  extern __shared__ uint8_t codes[];  // [tokens of the page][d]: values only
+// A code of a page whose scale grows from `was` to `scale`.
+__device__ __forceinline__ uint8_t recode(uint8_t code, float ratio) {
+  return (uint8_t)encode4(__builtin_amdgcn_cvt_f32_fp8((int)code, 0) * ratio, 0.f, 0.f, 0.f);
+}
+
+// x / scale: by its reciprocal where that is exact, which it is for every scale but those that others have set.
+struct Divide {
+  float scale, inv;
+  bool exact;
+  __device__ __forceinline__ explicit Divide(float s) : scale(s), inv(1.f / s), exact((__float_as_uint(s) & 0x7fffffu) == 0) {}
+  __device__ __forceinline__ float operator()(float x) const { return exact ? x * inv : x / scale; }
+};
+
+// The scale of a page whose new tokens reach `most` and whose older ones, if any, have the scale `was`.
+__device__ __forceinline__ float page_scale(float most, float was) {
+  const float least = least_scale(most);
+  return was > least ? was : least;  // a scale that is not a number is replaced
+}
+__device__ __forceinline__ float magnitude(float x) {
+  const float m = fabsf(x);
+  return m < __builtin_inff() ? m : 0.f;  // NaN and infinities do not set the scale
+}
+
+// One new token a sequence: a wave for each (sequence, head, keys or values), E = D / 64 elements a lane, all in
+// registers.  Bound by latency: the token is asked for before its page is known.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void cache_store_one_kernel(CacheStoreParams p) {
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (unit >= (int64_t)p.n_seqs * p.h_kv * 2) return;
+  const int side = (int)(unit & 1), n = (int)((unit >> 1) / p.h_kv), head = (int)((unit >> 1) - (int64_t)n * p.h_kv);
+  const T* x = reinterpret_cast<const T*>(side ? p.v : p.k) + n * (side ? p.v_stride : p.k_stride) + head * D + lane * E;
+  float f[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) f[e] = to_f32(x[e]);
+  const int held = as_const(p.lens)[n];
+  if (held < 0 || held / p.page >= p.max_pages) return;
+  const int pid = as_const(p.page_table)[(int64_t)n * p.max_pages + held / p.page];
+  if (pid < 0 || pid >= p.pages) return;
+  const int a = held % p.page;
+  float* scale_at = (side ? p.v_scale : p.k_scale) + (int64_t)pid * p.h_kv + head;
+  const float was = a > 0 ? *scale_at : 0.f;
+  float most = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) most = fmaxf(most, magnitude(f[e]));
+  most = block_max<64>(most);
+  const float scale = page_scale(most, was);
+  const Divide by(scale);
+  uint8_t* out = (side ? p.v_cache : p.k_cache) + ((int64_t)pid * p.h_kv + head) * D * p.page + (side ? lane * E * p.page : lane * E);
+  const int step = side ? 1 : D, next = side ? p.page : 1;  // from token to token, from element to element
+  if (a > 0 && scale != was) {
+    const float ratio = was / scale;
+    for (int t = 0; t < a; ++t)
+#pragma unroll
+      for (int e = 0; e < E; ++e) out[t * step + e * next] = recode(out[t * step + e * next], ratio);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) f[e] = by(f[e]);
+  const uint32_t w = encode4(f[0], E > 1 ? f[E > 1 ? 1 : 0] : 0.f, E > 2 ? f[E > 2 ? 2 : 0] : 0.f, E > 3 ? f[E > 3 ? 3 : 0] : 0.f);
+  uint8_t* at = out + a * step;
+  if (side) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) at[e * p.page] = (uint8_t)(w >> (8 * e));
+  } else if constexpr (E == 4) {
+    *reinterpret_cast<uint32_t*>(at) = w;
+  } else if constexpr (E == 2) {
+    *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+  } else {
+    *at = (uint8_t)w;
+  }
+  if (lane == 0) *scale_at = scale;
+}
+
+// Any number of new tokens: a workgroup for each (page, head, keys or values).  The values read for the maximum
+// stay in registers up to kKeep pieces of 8 a thread (a page of 64 tokens of 256); what is beyond is read again.
+constexpr int kKeep = 8;
+template <typename T>
+__global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreParams p) {
+  extern __shared__ uint8_t codes[];  // [tokens of the page][d + 4]: values only
   const int tid = threadIdx.x, head = blockIdx.y, side = blockIdx.z;
   int n, j;
   find_slot(p, blockIdx.x, n, j);
@@ -89,68 +166,95 @@ __global__ __launch_bounds__(THREADS) void cache_store_kernel(CacheStoreParams p
   const int a = (int)max(held - first, (int64_t)0);
   const int b = (int)min(held + (end - begin) - first, (int64_t)p.page);
   const int64_t row = begin + first + a - held;
-  const int d = p.d, per = d / 8;  // 8 elements a thread
+  const int d = p.d, shift = d == 256 ? 5 : d == 128 ? 4 : 3, per = d / 8;  // pieces of 8 elements, 2^shift a token
   const T* x = reinterpret_cast<const T*>(side ? p.v : p.k) + row * (side ? p.v_stride : p.k_stride) + head * d;
   const int64_t stride = side ? p.v_stride : p.k_stride;
+  const int count = (b - a) * per;
+  auto load = [&](int i, float (&f)[8]) { load8(x + (i >> shift) * stride + (i & (per - 1)) * 8, f); };
 
-  float most = 0.f;
-  for (int i = tid; i < (b - a) * per; i += THREADS) {
-    const int t = i / per, c = (i - t * per) * 8;
-    float f[8];
-    load8(x + t * stride + c, f);
+  float kept[kKeep][8], most = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float m = fabsf(f[e]);
-      most = fmaxf(most, m < __builtin_inff() ? m : 0.f);  // NaN and infinities do not set the scale
-    }
+  for (int k = 0; k < kKeep; ++k)
+    if (tid + 256 * k < count) load(tid + 256 * k, kept[k]);
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (tid + 256 * k < count)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, magnitude(kept[k][e]));
+  for (int i = tid + 256 * kKeep; i < count; i += 256) {
+    float f[8];
+    load(i, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, magnitude(f[e]));
   }
   float* scale_at = (side ? p.v_scale : p.k_scale) + (int64_t)pid * p.h_kv + head;
   const float was = a > 0 ? *scale_at : 0.f;
-  most = block_max<THREADS>(most);
-  const float least = least_scale(most);
-  const float scale = was > least ? was : least;  // a scale that is not a number is replaced
-  const float inv = 1.f / scale;  // exact, unless the page's scale was set by others
+  const float scale = page_scale(block_max<256>(most), was);
+  const Divide by(scale);
   uint8_t* out = (side ? p.v_cache : p.k_cache) + ((int64_t)pid * p.h_kv + head) * d * p.page;
 
   if (a > 0 && scale != was) {  // the page's older tokens, by the new scale
-    const float ratio = was * inv;
-    for (int i = tid; i < a * d; i += THREADS) {
+    const float ratio = was / scale;
+    for (int i = tid; i < a * d; i += 256) {
       const int t = i / d, c = i - t * d;
       uint8_t* at = out + (side ? c * p.page + t : i);
-      const float old = __builtin_amdgcn_cvt_f32_fp8((int)*at, 0);
-      *at = (uint8_t)encode4(old * ratio, 0.f, 0.f, 0.f);
+      *at = recode(*at, ratio);
     }
   }
-  for (int i = tid; i < (b - a) * per; i += THREADS) {
-    const int t = i / per, c = (i - t * per) * 8;
-    float f[8];
-    load8(x + t * stride + c, f);
+  auto put = [&](int i, float (&f)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= inv;
-    uint2 w;
-    w.x = encode4(f[0], f[1], f[2], f[3]);
-    w.y = encode4(f[4], f[5], f[6], f[7]);
-    *reinterpret_cast<uint2*>(side ? codes + t * d + c : out + (int64_t)(a + t) * d + c) = w;
+    for (int e = 0; e < 8; ++e) f[e] = by(f[e]);
+    const uint32_t lo = encode4(f[0], f[1], f[2], f[3]), hi = encode4(f[4], f[5], f[6], f[7]);
+    const int t = i >> shift, c = (i & (per - 1)) * 8;
+    if (side) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(codes + t * (d + 4) + c);
+      at[0] = lo;
+      at[1] = hi;
+    } else {
+      *reinterpret_cast<uint2*>(out + (a + t) * d + c) = make_uint2(lo, hi);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (tid + 256 * k < count) put(tid + 256 * k, kept[k]);
+  for (int i = tid + 256 * kKeep; i < count; i += 256) {
+    float f[8];
+    load(i, f);
+    put(i, f);
   }
-  __syncthreads();
+  __syncthreads();  // (every thread has read the page's scale)
   if (tid == 0) *scale_at = scale;
   if (!side) return;
-  // values: 16 neighbouring slots of one element a turn, bytes where the new tokens end inside them
+  // Values turned round: a thread takes 4 elements of 16 neighbouring slots, 16 words from LDS, and turns them 4 by
+  // 4 bytes; neighbouring threads have an element's next slots, so that they write whole rows of a page together.
+  // Rows of d + 4 bytes keep their reads in different banks.
   const int g0 = a / 16, groups = (b + 15) / 16 - g0;
-  for (int i = tid; i < groups * d; i += THREADS) {
-    const int c = i % d, s0 = (g0 + i / d) * 16;
-    uint8_t* at = out + (int64_t)c * p.page + s0;
+  for (int i = tid; i < groups * (d / 4); i += 256) {
+    const int c = i / groups * 4, s0 = (g0 + i % groups) * 16;
+    uint8_t* at = out + c * p.page + s0;
     if (s0 >= a && s0 + 16 <= b) {
-      uint32_t w[4];
+      uint32_t r[4][4];  // [element][slots / 4]
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        w[q] = 0;
+        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[q] |= (uint32_t)codes[(s0 - a + 4 * q + e) * d + c] << (8 * e);
+        for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(codes + (s0 - a + 4 * q + e) * (d + 4) + c);
+        // 4 x 4 bytes: first and second halves of the words' pairs, then their bytes
+        const uint32_t p0 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400), p1 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400);
+        const uint32_t p2 = __builtin_amdgcn_perm(w[1], w[0], 0x07030602), p3 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602);
+        r[0][q] = __builtin_amdgcn_perm(p1, p0, 0x05040100);
+        r[1][q] = __builtin_amdgcn_perm(p1, p0, 0x07060302);
+        r[2][q] = __builtin_amdgcn_perm(p3, p2, 0x05040100);
+        r[3][q] = __builtin_amdgcn_perm(p3, p2, 0x07060302);
       }
-      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(at + e * p.page) = make_uint4(r[e][0], r[e][1], r[e][2], r[e][3]);
     } else {
-      for (int e = max(0, a - s0); e < min(16, b - s0); ++e) at[e] = codes[(s0 - a + e) * d + c];
+      for (int t = max(0, a - s0); t < min(16, b - s0); ++t) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (s0 - a + t) * (d + 4) + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) at[e * p.page + t] = (uint8_t)(w >> (8 * e));
+      }
     }
   }
 }
@@ -164,13 +268,16 @@ hipError_t launch(CacheStoreParams p, hipStream_t stream) {
     p.uniform = p.tokens / p.n_seqs;
     p.uniform_slots = (int32_t)((p.uniform + p.page - 2) / p.page + 1);
     slots = (int64_t)p.uniform_slots * p.n_seqs;
+    if (p.uniform == 1) {
+      const dim3 grid((unsigned)(((int64_t)p.n_seqs * p.h_kv * 2 + 3) / 4));
+      if (p.d == 64) hipLaunchKernelGGL((cache_store_one_kernel<T, 64>), grid, dim3(256), 0, stream, p);
+      else if (p.d == 128) hipLaunchKernelGGL((cache_store_one_kernel<T, 128>), grid, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL((cache_store_one_kernel<T, 256>), grid, dim3(256), 0, stream, p);
+      return hipGetLastError();
+    }
   }
-  const dim3 grid((unsigned)slots, (unsigned)p.h_kv, 2);
-  // a page's new tokens at most: what of it passes through LDS
-  const bool one = !p.cu_seqlens && p.uniform == 1;
-  const size_t lds = (size_t)(one ? 1 : p.page) * p.d;
-  if (one) hipLaunchKernelGGL((cache_store_kernel<T, 64>), grid, dim3(64), lds, stream, p);
-  else hipLaunchKernelGGL((cache_store_kernel<T, 256>), grid, dim3(256), lds, stream, p);
+  const size_t lds = (size_t)p.page * (p.d + 4);
+  hipLaunchKernelGGL((cache_store_kernel<T>), dim3((unsigned)slots, (unsigned)p.h_kv, 2), dim3(256), lds, stream, p);
   return hipGetLastError();
 }
 
