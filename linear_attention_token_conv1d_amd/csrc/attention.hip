@@ -143,11 +143,7 @@ __device__ __forceinline__ Tile find_tile(const AttendParams& p, int slot, int g
   } else {
     // sequence n has the slots from cu[n] group / tile_rows + n on: at least as many as its tiles
     cint32* cu = as_const(p.cu_seqlens);
-    int lo = 0, hi = p.n_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)cu[mid] * group / tile_rows + mid <= slot) lo = mid; else hi = mid - 1;
-    }
+    const int lo = find_sequence(p.cu_seqlens, p.n_seqs, slot, [&](int64_t c, int n) { return c * group / tile_rows + n; });
     t.n = lo;
     j = slot - (int)((int64_t)cu[lo] * group / tile_rows + lo);
     t.begin = max(cu[lo], 0);

@@ -9,8 +9,8 @@
 // fall among e4m3's subnormals.  (e4m3 keeps four bits at any size, so a scale
 // between two powers of two would not make its values more exact.)
 //
-// One workgroup owns one (page, head) of the keys or the values, so the
-// page's maximum, its scale and its older tokens need no atomics and no second
+// One workgroup owns one (page, head) of the keys or the values, so the page's
+// maximum, its scale and its older tokens need no atomics and no second
 // launch.  Bound by bytes for long prompts (the values read, a code each
 // written) and by latency for single tokens.  Keys lie [token][d] in a page,
 // values [d][token]: attention then reads both with 16-byte loads in the order
@@ -61,14 +61,8 @@ __device__ __forceinline__ void find_slot(const CacheStoreParams& p, int slot, i
     j = slot - n * p.uniform_slots;
     return;
   }
-  cint32* cu = as_const(p.cu_seqlens);
-  int lo = 0, hi = p.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu[mid] / p.page + 2 * mid <= slot) lo = mid; else hi = mid - 1;
-  }
-  n = lo;
-  j = slot - (cu[lo] / p.page + 2 * lo);
+  n = find_sequence(p.cu_seqlens, p.n_seqs, slot, [&](int64_t c, int i) { return c / p.page + 2 * (int64_t)i; });
+  j = slot - (as_const(p.cu_seqlens)[n] / p.page + 2 * n);
 }
 
 // A code of a page whose scale grows from `was` to `scale`.
@@ -145,6 +139,33 @@ __global__ __launch_bounds__(256) void cache_store_one_kernel(CacheStoreParams p
   if (lane == 0) *scale_at = scale;
 }
 
+// Eight elements as they lie in memory, and the largest magnitude among them as an ordered whole number: two bf16 at a
+// time, or fp32 bits.  Infinities and NaN are the largest of all, so a page without them shows that by its maximum.
+template <typename T> struct Piece;
+template <> struct alignas(16) Piece<__bf16> {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  static constexpr uint32_t kNotFinite = 0x7f800000u;
+  uint32_t w[4];
+  __device__ __forceinline__ float get(int e) const { return e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]); }
+  __device__ __forceinline__ void reach(uint32_t& most) const {
+    u16x2 m = __builtin_bit_cast(u16x2, most);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+    most = __builtin_bit_cast(uint32_t, m);
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t most) { return max(most << 16, most & 0xffff0000u); }  // as fp32
+};
+template <> struct alignas(16) Piece<float> {
+  static constexpr uint32_t kNotFinite = 0x7f800000u;
+  float v[8];
+  __device__ __forceinline__ float get(int e) const { return v[e]; }
+  __device__ __forceinline__ void reach(uint32_t& most) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7fffffffu);
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t most) { return most; }
+};
+
 // Any number of new tokens: a workgroup for each (page, head, keys or values).  The values read for the maximum
 // stay in registers up to kKeep pieces of 8 a thread (a page of 64 tokens of 256); what is beyond is read again.
 constexpr int kKeep = 8;
@@ -160,36 +181,42 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreParams p) {
   if (held < 0 || end <= begin) return;
   const int64_t first = (held / p.page + j) * p.page;  // the page's first position
   if (first >= held + (end - begin) || first / p.page >= p.max_pages) return;
-  const int pid = as_const(p.page_table)[(int64_t)n * p.max_pages + first / p.page];
-  if (pid < 0 || pid >= p.pages) return;
   // slots [a, b) of the page get the tokens from row on
   const int a = (int)max(held - first, (int64_t)0);
   const int b = (int)min(held + (end - begin) - first, (int64_t)p.page);
   const int64_t row = begin + first + a - held;
   const int d = p.d, shift = d == 256 ? 5 : d == 128 ? 4 : 3, per = d / 8;  // pieces of 8 elements, 2^shift a token
+  const int count = (b - a) * per;
   const T* x = reinterpret_cast<const T*>(side ? p.v : p.k) + row * (side ? p.v_stride : p.k_stride) + head * d;
   const int64_t stride = side ? p.v_stride : p.k_stride;
-  const int count = (b - a) * per;
-  auto load = [&](int i, float (&f)[8]) { load8(x + (i >> shift) * stride + (i & (per - 1)) * 8, f); };
-
-  float kept[kKeep][8], most = 0.f;
+  auto load = [&](int i) { return *reinterpret_cast<const Piece<T>*>(x + (i >> shift) * stride + (i & (per - 1)) * 8); };
+  Piece<T> kept[kKeep];
 #pragma unroll
   for (int k = 0; k < kKeep; ++k)
-    if (tid + 256 * k < count) load(tid + 256 * k, kept[k]);
-#pragma unroll
-  for (int k = 0; k < kKeep; ++k)
-    if (tid + 256 * k < count)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = fmaxf(most, magnitude(kept[k][e]));
-  for (int i = tid + 256 * kKeep; i < count; i += 256) {
-    float f[8];
-    load(i, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) most = fmaxf(most, magnitude(f[e]));
-  }
+    if (tid + 256 * k < count) kept[k] = load(tid + 256 * k);
+  const int pid = as_const(p.page_table)[(int64_t)n * p.max_pages + first / p.page];
+  if (pid < 0 || pid >= p.pages) return;
   float* scale_at = (side ? p.v_scale : p.k_scale) + (int64_t)pid * p.h_kv + head;
   const float was = a > 0 ? *scale_at : 0.f;
-  const float scale = page_scale(block_max<256>(most), was);
+
+  uint32_t bits = 0;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (tid + 256 * k < count) kept[k].reach(bits);
+  for (int i = tid + 256 * kKeep; i < count; i += 256) load(i).reach(bits);
+  // (whole numbers below 2^31 keep their order as fp32 bits, but NaN's would not: they go by their own flag)
+  bits = Piece<T>::bits(bits);
+  const bool wild = __syncthreads_or(bits >= Piece<T>::kNotFinite);
+  if (wild) {  // infinities and NaN do not set the scale
+    float most = 0.f;
+    for (int i = tid; i < count; i += 256) {
+      const Piece<T> f = load(i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, magnitude(f.get(e)));
+    }
+    bits = __float_as_uint(most);
+  }
+  const float scale = page_scale(block_max<256>(__uint_as_float(bits)), was);
   const Divide by(scale);
   uint8_t* out = (side ? p.v_cache : p.k_cache) + ((int64_t)pid * p.h_kv + head) * d * p.page;
 
@@ -201,10 +228,19 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreParams p) {
       *at = recode(*at, ratio);
     }
   }
-  auto put = [&](int i, float (&f)[8]) {
+  auto put = [&](int i, const Piece<T>& piece) {
+    float f[8];
+    uint32_t lo, hi;
+    if (!wild && by.exact) {  // all within the range
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = by(f[e]);
-    const uint32_t lo = encode4(f[0], f[1], f[2], f[3]), hi = encode4(f[4], f[5], f[6], f[7]);
+      for (int e = 0; e < 8; ++e) f[e] = piece.get(e) * by.inv;
+      lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false), true);
+      hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false), true);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = by(piece.get(e));
+      lo = encode4(f[0], f[1], f[2], f[3]), hi = encode4(f[4], f[5], f[6], f[7]);
+    }
     const int t = i >> shift, c = (i & (per - 1)) * 8;
     if (side) {
       uint32_t* at = reinterpret_cast<uint32_t*>(codes + t * (d + 4) + c);
@@ -217,12 +253,8 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreParams p) {
 #pragma unroll
   for (int k = 0; k < kKeep; ++k)
     if (tid + 256 * k < count) put(tid + 256 * k, kept[k]);
-  for (int i = tid + 256 * kKeep; i < count; i += 256) {
-    float f[8];
-    load(i, f);
-    put(i, f);
-  }
-  __syncthreads();  // (every thread has read the page's scale)
+  for (int i = tid + 256 * kKeep; i < count; i += 256) put(i, load(i));
+  __syncthreads();  // every thread has read the page's scale; the values' codes are in LDS
   if (tid == 0) *scale_at = scale;
   if (!side) return;
   // Values turned round: a thread takes 4 elements of 16 neighbouring slots, 16 words from LDS, and turns them 4 by
