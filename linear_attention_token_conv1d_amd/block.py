@@ -82,16 +82,29 @@ def declare(L):
         f.restype = ctypes.c_size_t
 
 
+_SIZE = {c: ctypes.sizeof(c) for c in (NormArgs, NormBwdArgs, RopeArgs, CacheStoreArgs, CacheAttentionArgs)}
+_stream_of = torch._C._cuda_getCurrentRawStream
+_device_now = torch._C._cuda_getDevice
+_entries = {}
+
+
+def _entry(name):
+    f = _entries.get(name)
+    if f is None:
+        f = _entries[name] = getattr(lib(), name)
+    return f
+
+
 def _run(name, args, index):
     """Call an entry point on the current stream of GPU `index`."""
-    L = lib()
-    f = getattr(L, name)
-    if index == torch.cuda.current_device():
-        status = f(args, torch._C._cuda_getCurrentRawStream(index))
+    f = _entry(name)
+    if index == _device_now():
+        status = f(args, _stream_of(index))
     else:
         with torch.cuda.device(index):
-            status = f(args, torch._C._cuda_getCurrentRawStream(index))
+            status = f(args, _stream_of(index))
     if status:
+        L = lib()
         raise GdnError(f"{name}: {L.gdn_status_string(status).decode()}: {L.gdn_last_error().decode()}")
 
 
@@ -101,16 +114,23 @@ def _gpu(t, name):
     return t.get_device()
 
 
+def _wrong(t, name, index, shape, dtype):
+    """What is wrong with a tensor that is not on GPU `index`, or not of this dtype or shape."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        return GdnError(f"{name} must be on the same GPU as the call's other tensors")
+    if t.dtype != dtype:
+        return GdnError(f"{name} must be {dtype}, got {t.dtype}")
+    return GdnError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
 def _tensor(t, name, index, shape, dtype):
     """An optional contiguous tensor of exactly this shape and dtype on GPU `index`: its address."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.get_device() != index:
-        raise GdnError(f"{name} must be on the same GPU as the call's other tensors")
-    if t.dtype != dtype:
-        raise GdnError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise GdnError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        raise _wrong(t, name, index, shape, dtype)
+    if not t.is_contiguous():
+        raise GdnError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
@@ -118,12 +138,8 @@ def _rows(t, name, index, shape, dtype):
     """An optional [T, H, d] or [T, d] tensor, token stride free: its address and token stride."""
     if t is None:
         return None, 0
-    if not isinstance(t, torch.Tensor) or t.get_device() != index:
-        raise GdnError(f"{name} must be on the same GPU as the call's other tensors")
-    if t.dtype is not dtype:
-        raise GdnError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise GdnError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        raise _wrong(t, name, index, shape, dtype)
     if t.is_contiguous():
         return t.data_ptr(), shape[1] if len(shape) == 2 else shape[1] * shape[2]
     s = t.stride()
@@ -179,7 +195,7 @@ def rms_norm(x, weight=None, gate=None, residual=None, order="pre", activation="
     py, sy = _rows(y, "out", index, shape, dt)
     ps, ss = _rows(sum_out, "sum_out", index, shape, dt)
     pw = _tensor(weight, "weight", index, (width,), weight.dtype) if weight is not None else None
-    a = NormArgs(ctypes.sizeof(NormArgs), _DT[dt], F32 if weight is None else _DT[weight.dtype], order, act, heads, width,
+    a = NormArgs(_SIZE[NormArgs], _DT[dt], F32 if weight is None else _DT[weight.dtype], order, act, heads, width,
                  eps, scale, weight_offset, shape[0], px, pw, pg, pr, py, ps, sx, sg, sr, sy, ss)
     _run("gdn_rms_norm", a, index)
     return (y, sum_out) if sums else y
@@ -220,11 +236,11 @@ def rms_norm_backward(x, dy, weight=None, gate=None, d_sum=None, residual=False,
     if weight is not None:
         pw = _tensor(weight, "weight", index, (width,), weight.dtype)
         dweight = torch.empty(width, dtype=torch.float32, device=dev)
-    a = NormBwdArgs(ctypes.sizeof(NormBwdArgs), _DT[dt], F32 if weight is None else _DT[weight.dtype], order, act, heads,
+    a = NormBwdArgs(_SIZE[NormBwdArgs], _DT[dt], F32 if weight is None else _DT[weight.dtype], order, act, heads,
                     width, eps, scale, weight_offset, shape[0], px, pw, pg, pd, pu, po, pr, pz,
                     None if dweight is None else dweight.data_ptr(), sx, sg, sd, su, so, sr, sz)
     if dweight is not None:
-        workspace = _workspace(workspace, lib().gdn_rms_norm_backward_workspace_size(a), index, dev)
+        workspace = _workspace(workspace, _entry("gdn_rms_norm_backward_workspace_size")(a), index, dev)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
     _run("gdn_rms_norm_backward", a, index)
     return dx, dres, dweight, dgate
@@ -310,7 +326,7 @@ def _rope(q, positions, inv_freq, k, layout, mscale, inverse, out, k_out):
         pz, sz = _rows(z, "k_out", index, k.shape, dt)
     elif k_out is not None:
         raise GdnError("k_out goes with k")
-    a = RopeArgs(ctypes.sizeof(RopeArgs), _DT[dt], ROPE_LAYOUT[layout], inverse, 64 if positions.dtype == torch.int64 else 32,
+    a = RopeArgs(_SIZE[RopeArgs], _DT[dt], ROPE_LAYOUT[layout], inverse, 64 if positions.dtype == torch.int64 else 32,
                  h_q, h_k, d, 2 * inv_freq.shape[0], mscale, T, pq, pk, pp, pf, py, pz, sq, sk, sy, sz)
     _run("gdn_rope", a, index)
     return y if k is None else (y, z)
@@ -392,7 +408,7 @@ def cache_store(k, v, cache, page_table, lens, cu_seqlens=None):
     pv, sv = _rows(v, "v", index, k.shape, k.dtype)
     pages, page, pkc, pvc, pks, pvs = _cache(cache, index, h, d)
     n, width, pt, pl, pc = _sequences(page_table, lens, cu_seqlens, index, T)
-    a = CacheStoreArgs(ctypes.sizeof(CacheStoreArgs), _DT[k.dtype], n, h, d, page, pages, width, T, pk, pv, sk, sv, pkc, pvc, pks, pvs,
+    a = CacheStoreArgs(_SIZE[CacheStoreArgs], _DT[k.dtype], n, h, d, page, pages, width, T, pk, pv, sk, sv, pkc, pvc, pks, pvs,
                        pt, pl, pc)
     _run("gdn_cache_store", a, index)
 
@@ -425,10 +441,10 @@ def cache_attention(q, cache, page_table, lens, cu_seqlens=None, scale=None, cau
     o = torch.empty_like(q) if out is None else out
     po, so = _rows(o, "out", index, q.shape, dt)
     lse = torch.empty((T, h_q), dtype=torch.float32, device=q.device) if return_lse else None
-    a = CacheAttentionArgs(ctypes.sizeof(CacheAttentionArgs), _DT[dt], n, h_q, h, d, page, pages, width, 1 if causal else 0, window,
+    a = CacheAttentionArgs(_SIZE[CacheAttentionArgs], _DT[dt], n, h_q, h, d, page, pages, width, 1 if causal else 0, window,
                            d ** -0.5 if scale is None else scale, T, pq, pg, po, sq, sg, so, None if lse is None else lse.data_ptr(), pkc,
                            pvc, pks, pvs, pt, pl, pc)
-    need = lib().gdn_cache_attention_workspace_size(a)
+    need = _entry("gdn_cache_attention_workspace_size")(a)
     if need or workspace is not None:
         workspace = _workspace(workspace, need, index, q.device)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
