@@ -842,7 +842,6 @@ __global__ __launch_bounds__(256) void join_kernel(AttendParams p) {
       ll += a * p.part_ml[2 * part + 1];
     }
     const int n = min(64, ns - s0);
-#pragma unroll 4
     for (int s = 0; s < n; ++s) {
       const float as = __shfl(a, s, 64);
       const float* row = p.part_o + ((s0 + s) * step + out) * D + lane * E;
