@@ -584,7 +584,7 @@ gdn_status gdn_rms_norm_backward(const gdn_rms_norm_backward_args* args, void* s
  *   inv_freq     [rot / 2] fp64 radians a position: scaled as a long-context
  *                scheme asks, if any; mscale is such a scheme's factor on the
  *                cosines and sines (1 otherwise).
- *   h_q, h_k     heads; h_k = 0 without k.   d >= 2, rot even, 2..d.
+ *   h_q, h_k     heads; h_k = 0 without k.   d 2..16384, rot even, 2..d.
  *   q, q_out     [tokens, h_q, d], k, k_out [tokens, h_k, d] with token
  *                strides in elements (heads contiguous inside a token).  16-byte
  *                accesses are used where pointers, strides, d and rot allow

@@ -224,7 +224,7 @@ gdn_status gdn_rope(const gdn_rope_args* a, void* stream) {
     if (a->position_bits != 32 && a->position_bits != 64) return fail(GDN_ERR_INVALID_ARG, "%s: position_bits is 32 or 64", f);
     if (a->h_q < 1 || a->h_k < 0 || a->h_q > 65535 || a->h_k > 65535)
       return fail(GDN_ERR_INVALID_ARG, "%s: h_q in 1..65535 and h_k in 0..65535 required", f);
-    if (a->d < 2 || a->d > 65536) return fail(GDN_ERR_INVALID_ARG, "%s: d %d not in 2..65536", f, a->d);
+    if (a->d < 2 || a->d > 16384) return fail(GDN_ERR_INVALID_ARG, "%s: d %d not in 2..16384", f, a->d);
     if (a->rot < 2 || a->rot % 2 || a->rot > a->d) return fail(GDN_ERR_INVALID_ARG, "%s: rot %d is not even in 2..d", f, a->rot);
     if (!std::isfinite(a->mscale)) return fail(GDN_ERR_INVALID_ARG, "%s: bad mscale", f);
     if (a->tokens < 0 || a->tokens > INT32_MAX) return fail(GDN_ERR_INVALID_ARG, "%s: tokens out of range", f);
@@ -260,7 +260,7 @@ gdn_status gdn_rope(const gdn_rope_args* a, void* stream) {
     }
     gdn::RopeParams p{a->q, a->k, a->positions, a->inv_freq, a->q_out, a->k_out, a->q_stride, a->k_stride,
                       a->q_out_stride, a->k_out_stride, a->tokens, a->position_bits == 64 ? 1 : 0, a->h_q, a->h_k, a->d,
-                      a->rot, a->layout == GDN_ROPE_HALF ? 1 : 0, a->inverse, a->mscale, 0, 0, 0};
+                      a->rot, a->layout == GDN_ROPE_HALF ? 1 : 0, a->inverse, a->mscale, 0};
     hipStream_t s = static_cast<hipStream_t>(stream);
     return finish(gdn::launch_rope(p, a->dtype, s), s, f);
   } catch (...) {

@@ -222,10 +222,7 @@ struct RopeParams {
   int32_t half;
   int32_t inverse;
   float mscale;
-  // set by the launcher: units of a head, head groups of a token, heads of a group
-  int32_t units;
-  int32_t splits;
-  int32_t per;
+  int32_t units;  // of a head: set by the launcher
 };
 hipError_t launch_rope(const RopeParams& p, int dtype, hipStream_t stream);
 

@@ -6,10 +6,14 @@
 // over the pairs (i, i + rot/2) of a head (half layout) or (2i, 2i + 1)
 // (interleaved layout); elements from rot on pass through.
 //
-// Bound by the bytes of q and k.  A thread owns the same elements of every
-// head it visits: the angle is formed once for a token and pair and used for
-// all of them, so the trigonometry costs next to nothing and no table of
-// sines is read.  The angle is reduced in fp64 turns, position * inv_freq /
+// Bound by the bytes of q and k, which neighbouring threads read and write in
+// the order they lie in.  A thread has one piece of one head and forms its
+// angles itself: no table of sines is read, and the arithmetic hides behind
+// the bytes.  (Threads that take their piece of several heads share the
+// angles among those but jump from head to head: 65536 tokens of 28 heads of
+// 256 took 410 us with all heads a thread, 372 with four, 341 with one; fp32
+// heads of 128 rotated whole 134, 119 and 117.)
+// The angle is reduced in fp64 turns, position * inv_freq /
 // 2 pi minus its nearest whole number, exact to 2^-53 of the unreduced angle
 // (an fp32 product would be a tenth of a radian off at position 2^20).  Sine
 // and cosine of the reduced turn are then fp32: the hardware's for bf16
@@ -51,94 +55,87 @@ __device__ __forceinline__ void store_span(T* p, const Span<T, N>& s) {
   *reinterpret_cast<Span<T, N>*>(p) = s;
 }
 
+// This thread's token, head (the keys' behind the queries') and unit of the head.
+struct Place {
+  int64_t t;
+  int unit;
+  bool some;
+  const void* src;
+  void* dst;
+};
+template <typename T>
+__device__ __forceinline__ Place place(const RopeParams& p) {
+  Place w;
+  const uint32_t id = blockIdx.x * kThreads + threadIdx.x, row = id / (uint32_t)p.units, heads = (uint32_t)(p.h_q + p.h_k);
+  const uint32_t t = row / heads, h = row - t * heads;
+  w.unit = (int)(id - row * (uint32_t)p.units);
+  w.t = t;
+  w.some = t < p.tokens;
+  const bool is_q = h < (uint32_t)p.h_q;
+  const int64_t head = (int64_t)(is_q ? h : h - p.h_q) * p.d;
+  w.src = reinterpret_cast<const T*>(is_q ? p.q : p.k) + w.t * (is_q ? p.q_stride : p.k_stride) + head;
+  w.dst = reinterpret_cast<T*>(is_q ? p.q_out : p.k_out) + w.t * (is_q ? p.q_out_stride : p.k_out_stride) + head;
+  return w;
+}
+__device__ __forceinline__ double position(const RopeParams& p, int64_t t) {
+  return p.pos64 ? (double)reinterpret_cast<const int64_t*>(p.positions)[t] : (double)reinterpret_cast<const int32_t*>(p.positions)[t];
+}
+constexpr double kTurn = 0.15915494309189533577;  // 1 / 2 pi
+
 // A unit is 2 N elements of a head: N of the first and N of the second half
 // (half layout), 2 N neighbours (interleaved, and behind the rotated part).
-// A thread takes one unit of one token in `per` heads of the nq + nk.
 template <typename T, int N, bool HALF>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t job = id / p.units;  // token, then group of heads
-  const int unit = (int)(id - job * p.units);
-  const int64_t t = job / p.splits;
-  if (t >= p.tokens) return;
-  const int heads = p.h_q + p.h_k;
-  int h = (int)(job - t * p.splits) * p.per;
-  const int end = min(h + p.per, heads);
-  const int rot_units = p.rot / (2 * N);
-  const bool turned = unit < rot_units;
-  // offsets of the unit's two spans inside a head
-  const int a_at = turned ? (HALF ? unit * N : unit * 2 * N) : unit * 2 * N;
-  const int b_at = turned && HALF ? p.rot / 2 + unit * N : a_at + N;
-  float c[N], s[N];
+  const Place w = place<T>(p);
+  if (!w.some) return;
+  const bool turned = w.unit < p.rot / (2 * N);
+  // the unit's two spans
+  const int a_at = turned && HALF ? w.unit * N : w.unit * 2 * N, b_at = turned && HALF ? p.rot / 2 + w.unit * N : a_at + N;
+  const T* src = reinterpret_cast<const T*>(w.src);
+  T* dst = reinterpret_cast<T*>(w.dst);
+  float c[N], s[N];  // formed before the pieces are asked for: 342 us where asking first takes 350 (65536 tokens)
   if (turned) {
-    const double pos = p.pos64 ? (double)reinterpret_cast<const int64_t*>(p.positions)[t]
-                               : (double)reinterpret_cast<const int32_t*>(p.positions)[t];
+    const double pos = position(p, w.t);
     const float sign = p.inverse ? -1.f : 1.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      turn<T>(pos * (p.inv_freq[unit * N + i] * 0.15915494309189533577), p.mscale, sign, c[i], s[i]);
+    for (int i = 0; i < N; ++i) turn<T>(pos * (p.inv_freq[w.unit * N + i] * kTurn), p.mscale, sign, c[i], s[i]);
   }
-#pragma unroll 4
-  for (; h < end; ++h) {
-    const bool is_q = h < p.h_q;
-    const int64_t head = (int64_t)(is_q ? h : h - p.h_q) * p.d;
-    const T* src = reinterpret_cast<const T*>(is_q ? p.q : p.k) + t * (is_q ? p.q_stride : p.k_stride) + head;
-    T* dst = reinterpret_cast<T*>(is_q ? p.q_out : p.k_out) + t * (is_q ? p.q_out_stride : p.k_out_stride) + head;
-    Span<T, N> a = load_span<T, N>(src + a_at), b = load_span<T, N>(src + b_at);
-    if (turned) {
-      float x[2 * N];
+  Span<T, N> a = load_span<T, N>(src + a_at), b = load_span<T, N>(src + b_at);
+  if (turned) {
+    float x[2 * N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = to_f32(a.v[i]), x[N + i] = to_f32(b.v[i]);
+    for (int i = 0; i < N; ++i) x[i] = to_f32(a.v[i]), x[N + i] = to_f32(b.v[i]);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int ia = HALF ? i : 2 * i, ib = HALF ? N + i : 2 * i + 1;
-        const float u = x[ia], w = x[ib];
-        x[ia] = u * c[i] - w * s[i];
-        x[ib] = w * c[i] + u * s[i];
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) a.v[i] = from_f32<T>(x[i]), b.v[i] = from_f32<T>(x[N + i]);
+    for (int i = 0; i < N; ++i) {
+      const int ia = HALF ? i : 2 * i, ib = HALF ? N + i : 2 * i + 1;
+      const float u = x[ia], v = x[ib];
+      x[ia] = u * c[i] - v * s[i];
+      x[ib] = v * c[i] + u * s[i];
     }
-    store_span<T, N>(dst + a_at, a);
-    store_span<T, N>(dst + b_at, b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) a.v[i] = from_f32<T>(x[i]), b.v[i] = from_f32<T>(x[N + i]);
   }
+  store_span<T, N>(dst + a_at, a);
+  store_span<T, N>(dst + b_at, b);
 }
 
 // Any even rot and any d: one pair, or one element behind the rotated part.
 template <typename T, bool HALF>
 __global__ __launch_bounds__(kThreads) void rope_any_kernel(RopeParams p) {
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t job = id / p.units;
-  const int unit = (int)(id - job * p.units);
-  const int64_t t = job / p.splits;
-  if (t >= p.tokens) return;
-  const int heads = p.h_q + p.h_k;
-  int h = (int)(job - t * p.splits) * p.per;
-  const int end = min(h + p.per, heads);
-  const bool turned = unit < p.rot / 2;
-  const int a_at = turned ? (HALF ? unit : 2 * unit) : unit + p.rot / 2;
-  const int b_at = turned ? (HALF ? unit + p.rot / 2 : a_at + 1) : a_at;
-  float c = 1.f, s = 0.f;
-  if (turned) {
-    const double pos = p.pos64 ? (double)reinterpret_cast<const int64_t*>(p.positions)[t]
-                               : (double)reinterpret_cast<const int32_t*>(p.positions)[t];
-    turn<T>(pos * (p.inv_freq[unit] * 0.15915494309189533577), p.mscale, p.inverse ? -1.f : 1.f, c, s);
+  const Place w = place<T>(p);
+  if (!w.some) return;
+  const T* src = reinterpret_cast<const T*>(w.src);
+  T* dst = reinterpret_cast<T*>(w.dst);
+  if (w.unit >= p.rot / 2) {
+    dst[w.unit + p.rot / 2] = src[w.unit + p.rot / 2];
+    return;
   }
-#pragma unroll 4
-  for (; h < end; ++h) {
-    const bool is_q = h < p.h_q;
-    const int64_t head = (int64_t)(is_q ? h : h - p.h_q) * p.d;
-    const T* src = reinterpret_cast<const T*>(is_q ? p.q : p.k) + t * (is_q ? p.q_stride : p.k_stride) + head;
-    T* dst = reinterpret_cast<T*>(is_q ? p.q_out : p.k_out) + t * (is_q ? p.q_out_stride : p.k_out_stride) + head;
-    const T a = src[a_at], b = src[b_at];
-    if (turned) {
-      const float u = to_f32(a), w = to_f32(b);
-      dst[a_at] = from_f32<T>(u * c - w * s);
-      dst[b_at] = from_f32<T>(w * c + u * s);
-    } else {
-      dst[a_at] = a;
-    }
-  }
+  const int a_at = HALF ? w.unit : 2 * w.unit, b_at = HALF ? w.unit + p.rot / 2 : a_at + 1;
+  const float u = to_f32(src[a_at]), v = to_f32(src[b_at]);
+  float c, s;
+  turn<T>(position(p, w.t) * (p.inv_freq[w.unit] * kTurn), p.mscale, p.inverse ? -1.f : 1.f, c, s);
+  dst[a_at] = from_f32<T>(u * c - v * s);
+  dst[b_at] = from_f32<T>(v * c + u * s);
 }
 
 bool spans_ok(const void* p, int64_t stride, int n, size_t es) {
@@ -154,15 +151,21 @@ hipError_t launch(RopeParams p, hipStream_t stream) {
                     spans_ok(p.k_out, p.k_out_stride, N, sizeof(T));
   // in place, what passes through stays where it is
   p.units = wide ? (in_place ? p.rot : p.d) / (2 * N) : (in_place ? p.rot / 2 : p.d - p.rot / 2);
-  // heads to a thread: as many as leave the chip full (256 CUs of 2048 threads), to share the angles
-  const int heads = p.h_q + p.h_k;
-  int64_t splits = ((int64_t)256 * 2048 + p.tokens * p.units - 1) / (p.tokens * p.units);
-  if (splits > heads) splits = heads;
-  p.per = (int32_t)((heads + splits - 1) / splits);
-  p.splits = (heads + p.per - 1) / p.per;
-  const int64_t blocks = (p.tokens * p.splits * p.units + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks);
+  const int64_t per_token = (int64_t)(p.h_q + p.h_k) * p.units;
+  // thread numbers are 32-bit: a call of more runs its tokens in parts
+  const int64_t most = ((int64_t)0xffffffff - kThreads) / per_token;
+  if (p.tokens > most) {
+    RopeParams a = p, b = p;
+    a.tokens = most;
+    b.tokens = p.tokens - most;
+    b.positions = reinterpret_cast<const char*>(p.positions) + most * (p.pos64 ? 8 : 4);
+    b.q = reinterpret_cast<const T*>(p.q) + most * p.q_stride;
+    b.q_out = reinterpret_cast<T*>(p.q_out) + most * p.q_out_stride;
+    if (p.h_k) b.k = reinterpret_cast<const T*>(p.k) + most * p.k_stride, b.k_out = reinterpret_cast<T*>(p.k_out) + most * p.k_out_stride;
+    const hipError_t e = launch<T>(a, stream);
+    return e != hipSuccess ? e : launch<T>(b, stream);
+  }
+  const dim3 grid((unsigned)((p.tokens * per_token + kThreads - 1) / kThreads));
   if (wide && p.half) hipLaunchKernelGGL((rope_kernel<T, N, true>), grid, dim3(kThreads), 0, stream, p);
   else if (wide) hipLaunchKernelGGL((rope_kernel<T, N, false>), grid, dim3(kThreads), 0, stream, p);
   else if (p.half) hipLaunchKernelGGL((rope_any_kernel<T, true>), grid, dim3(kThreads), 0, stream, p);
