@@ -38,7 +38,6 @@
 #include "gdn_device.h"
 #include "gdn_internal.h"
 
-#include <cstdlib>
 #include <algorithm>
 #include <type_traits>
 
@@ -132,6 +131,23 @@ struct Tile {
   bool some;       // whether there is such a tile
 };
 
+// Tile j of a sequence whose number, first token, length and context are known.
+__device__ __forceinline__ Tile finish_tile(const AttendParams& p, Tile t, int j, int group, int tile_rows) {
+  t.rows = t.len * group;
+  t.first = j * tile_rows;
+  t.some = t.len > 0 && j >= 0 && t.first < t.rows;
+  t.ctx = min(t.ctx, p.max_tokens);  // contexts end with the table
+  if (!t.some) return t;
+  const int t0 = t.first / group, t1 = min(t.len - 1, (t.first + tile_rows - 1) / group);
+  t.hi = p.causal ? min(t.ctx, t.ctx - t.len + t1 + 1) : t.ctx;
+  t.all_hi = p.causal ? min(t.ctx, t.ctx - t.len + t0 + 1) : t.ctx;
+  t.all_lo = p.window ? t.ctx - t.len + t1 - p.window + 1 : 0;
+  t.lo = p.window ? max(0, t.ctx - t.len + t0 - p.window + 1) : 0;
+  t.lo &= ~(kTok - 1);
+  if (t.hi < t.lo) t.hi = t.lo;
+  return t;
+}
+
 __device__ __forceinline__ Tile find_tile(const AttendParams& p, int slot, int group, int tile_rows) {
   Tile t;
   int j;
@@ -149,19 +165,8 @@ __device__ __forceinline__ Tile find_tile(const AttendParams& p, int slot, int g
     t.begin = max(cu[lo], 0);
     t.len = (int)(min((int64_t)cu[lo + 1], p.tokens) - t.begin);
   }
-  t.rows = t.len * group;
-  t.first = j * tile_rows;
-  t.some = t.len > 0 && j >= 0 && t.first < t.rows;
-  t.ctx = min(as_const(p.lens)[t.n], p.max_tokens);  // contexts end with the table
-  if (!t.some) return t;
-  const int t0 = t.first / group, t1 = min(t.len - 1, (t.first + tile_rows - 1) / group);
-  t.hi = p.causal ? min(t.ctx, t.ctx - t.len + t1 + 1) : t.ctx;
-  t.all_hi = p.causal ? min(t.ctx, t.ctx - t.len + t0 + 1) : t.ctx;
-  t.all_lo = p.window ? t.ctx - t.len + t1 - p.window + 1 : 0;
-  t.lo = p.window ? max(0, t.ctx - t.len + t0 - p.window + 1) : 0;
-  t.lo &= ~(kTok - 1);
-  if (t.hi < t.lo) t.hi = t.lo;
-  return t;
+  t.ctx = as_const(p.lens)[t.n];
+  return finish_tile(p, t, j, group, tile_rows);
 }
 
 __device__ __forceinline__ int pieces(const AttendParams& p, const Tile& t) {
@@ -210,7 +215,69 @@ __device__ __forceinline__ void put(const AttendParams& p, f32x4 o, int64_t toke
   store4(reinterpret_cast<T*>(p.o) + token * p.o_stride + at, y);
 }
 
-template <typename T, int D>
+// 16 bytes that no other workgroup reads soon: nontemporal (a decode step of 64 sequences of up to 32768 tokens 386 ->
+// 364 us; fp32 queries, whose registers do not suffice, are the better without: 618 against 631).
+template <bool STREAM>
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
+  if constexpr (!STREAM) return *reinterpret_cast<const uint4*>(p);
+  const gdn_u4 w = __builtin_nontemporal_load(reinterpret_cast<const gdn_u4*>(p));
+  return make_uint4(w.x, w.y, w.z, w.w);
+}
+
+// Shares: where every sequence has the same number of new tokens, all work is one line of steps of 256 tokens, tile
+// after tile and head after head, and each of `shares` workgroups takes an equal length of it, whatever the
+// contexts' lengths are.  Every workgroup finds the tiles' places on the line for itself (one pass over the
+// lengths); the first leaves them for join_kernel.  A tile that several workgroups meet in has a partial result
+// from each, at number (tile + workgroup), which rises along the line.
+constexpr int kMostTiles = 2048;  // of a call that is cut into shares
+constexpr int kStep = kWaves * kTok;
+// (of fewer steps than workgroups each of the first gets one: every share in use has a step, so those that meet in a
+// tile are numbered one after another)
+__device__ __forceinline__ int64_t share_begin(const AttendParams& p, int64_t total, int64_t share) {
+  const int64_t n = min((int64_t)p.shares, total);
+  return min(share, n) * total / n;
+}
+__device__ __forceinline__ int share_of(const AttendParams& p, int64_t total, int64_t step) {
+  return (int)(((step + 1) * min((int64_t)p.shares, total) - 1) / total);
+}
+
+// s_place[i]: steps of the tiles before tile i; their total after the last.  Called by all of a workgroup's waves.
+__device__ __forceinline__ void place_tiles(const AttendParams& p, int group, int* s_place, int* s_sums) {
+  const int per = (p.slots + kWaves * 64 - 1) / (kWaves * 64), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int sum = 0;
+  for (int i = 0; i < per; ++i) {
+    const int slot = threadIdx.x * per + i;
+    if (slot >= p.slots) break;
+    Tile t;
+    t.n = slot / p.uniform_tiles;
+    t.len = (int)p.uniform;
+    t.ctx = p.lens[t.n];
+    t = finish_tile(p, t, slot - t.n * p.uniform_tiles, group, kRows);
+    s_place[slot] = sum;
+    sum += max(1, (t.hi - t.lo + kStep - 1) / kStep);
+  }
+  int before = sum;  // of this thread and those before it in its wave
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) {
+    const int v = __shfl_up(before, x, 64);
+    if (lane >= x) before += v;
+  }
+  if (lane == 63) s_sums[wave] = before;
+  __syncthreads();
+  before -= sum;
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k)
+    if (k < wave) before += s_sums[k];
+  for (int i = 0; i < per; ++i) {
+    const int slot = threadIdx.x * per + i;
+    if (slot >= p.slots) break;
+    s_place[slot] += before;
+    if (slot == p.slots - 1) s_place[p.slots] = before + sum;
+  }
+  __syncthreads();
+}
+
+template <typename T, int D, bool SHARES>
 __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int NQ = F32 ? 3 : 1;
@@ -223,23 +290,57 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
   bf16x8* s_q = reinterpret_cast<bf16x8*>(lds);
   float(*s_o)[kRows][D + 4] = reinterpret_cast<float(*)[kRows][D + 4]>(lds);
 
+  __shared__ int s_place[SHARES ? kMostTiles + 1 : 1], s_sums[kWaves];
   const int group = p.h_q / p.h_kv;
-  const int head = blockIdx.y, piece = blockIdx.z;
-  // workgroups go to the 8 XCDs in turn: every XCD gets pieces of every sequence, however unequal those are
-  const Tile tile = find_tile(p, (blockIdx.x + piece) % gridDim.x, group, kRows);
-  if (!tile.some) return;
-  const int ns = pieces(p, tile);
-  if (piece >= ns) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int kg = r >> 2, ki = r & 3;  // this lane's row of the keys' operand: token 16 kg + 4 tt + ki
+  const int in_page = (1 << p.page_shift) - 1;
+  auto inside = [&](int id) { return id >= 0 && id < p.pages ? id : 0; };
+
+  // what is left of this workgroup's share, in steps
+  int64_t at = 0, end = 1, total = 1;
+  if constexpr (SHARES) {
+    place_tiles(p, group, s_place, s_sums);
+    total = (int64_t)s_place[p.slots] * p.h_kv;
+    at = share_begin(p, total, blockIdx.x), end = share_begin(p, total, (int64_t)blockIdx.x + 1);
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i <= p.slots; i += kWaves * 64) p.places[i] = s_place[i];
+  }
+  while (at < end) {
+  int head = blockIdx.y, ns, start, stop;
+  int64_t piece = blockIdx.z;  // which partial result this is
+  Tile tile;
+  if constexpr (SHARES) {
+    int lo = 0, hi = p.slots - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((int64_t)s_place[mid] * p.h_kv <= at) lo = mid; else hi = mid - 1;
+    }
+    const int slot = __builtin_amdgcn_readfirstlane(lo);
+    const int steps = __builtin_amdgcn_readfirstlane(s_place[slot + 1] - s_place[slot]);
+    const int64_t rest = at - (int64_t)__builtin_amdgcn_readfirstlane(s_place[slot]) * p.h_kv;
+    head = (int)(rest / steps);
+    const int step = (int)(rest - (int64_t)head * steps), n = (int)min((int64_t)(steps - step), end - at);
+    tile = find_tile(p, slot, group, kRows);
+    start = tile.lo + step * kStep;
+    stop = min(tile.hi, start + n * kStep);
+    ns = n == steps ? 1 : 2;  // the whole tile, or a part of it
+    piece = (int64_t)slot * p.h_kv + head + blockIdx.x;
+    at += n;
+  } else {
+    at = end;
+    // workgroups go to the 8 XCDs in turn: every XCD gets pieces of every sequence, however unequal those are
+    tile = find_tile(p, (blockIdx.x + blockIdx.z) % gridDim.x, group, kRows);
+    if (!tile.some) return;
+    ns = pieces(p, tile);
+    if (piece >= ns) return;
+    start = tile.lo + (int)piece * p.piece;
+    stop = min(tile.hi, start + p.piece);
+  }
 
   // A wave's codes stay on their way: a tile's keys are asked for when the last tile's have been used, and so
   // are its values; its pages a tile before that.
-  const int start = tile.lo + piece * p.piece;
-  const int stop = min(tile.hi, start + p.piece);
   const int32_t* table = p.page_table + (int64_t)tile.n * p.max_pages;
-  const int in_page = (1 << p.page_shift) - 1;
-  const int kg = r >> 2, ki = r & 3;  // this lane's row of the keys' operand: token 16 kg + 4 tt + ki
-  auto inside = [&](int id) { return id >= 0 && id < p.pages ? id : 0; };
   // pages of this lane's 16 tokens as a row of the keys, and as a column of the scores
   auto page_of = [&](int token) { return token < stop ? table[token >> p.page_shift] : -1; };
   uint4 kc[4][D / 64], vc[MT];
@@ -248,14 +349,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
 #pragma unroll
     for (int b = 0; b < D / 64; ++b)
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) kc[tt][b] = *reinterpret_cast<const uint4*>(kp + tt * 4 * D + b * 64);
+      for (int tt = 0; tt < 4; ++tt) kc[tt][b] = load_codes<!F32>(kp + tt * 4 * D + b * 64);
   };
   auto load_values = [&](int k0, int ps) {
     const uint8_t* vp = p.v_cache + ((((int64_t)inside(ps) * p.h_kv + head) * D + r) << p.page_shift) + ((k0 + 16 * g) & in_page);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) vc[i] = *reinterpret_cast<const uint4*>(vp + ((i * 16) << p.page_shift));
+    for (int i = 0; i < MT; ++i) vc[i] = load_codes<!F32>(vp + ((i * 16) << p.page_shift));
   };
-  constexpr int kStep = kWaves * kTok;
   const int k_first = start + wave * kTok;
   int pk = page_of(k_first + 16 * kg), ps = page_of(k_first + 16 * g);
   int pk_next = page_of(k_first + kStep + 16 * kg), ps_next = page_of(k_first + kStep + 16 * g);
@@ -425,33 +525,35 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
     if (live && (turn ? wave < 2 : wave >= 2)) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        f32x4* at = reinterpret_cast<f32x4*>(&s_o[wave & 1][r][i * 16 + g * 4]);
-        *at = turn ? *at + o[i] : o[i];
+        f32x4* sum = reinterpret_cast<f32x4*>(&s_o[wave & 1][r][i * 16 + g * 4]);
+        *sum = turn ? *sum + o[i] : o[i];
       }
     }
     __syncthreads();
   }
   for (int i = threadIdx.x; i < kRows * D / 4; i += kWaves * 64) {
-    const int rr = i / (D / 4), c = (i - rr * (D / 4)) * 4, at = tile.first + rr;
-    if (at >= tile.rows) break;
+    const int rr = i / (D / 4), c = (i - rr * (D / 4)) * 4, out_row = tile.first + rr;
+    if (out_row >= tile.rows) break;
     float top = s_m[0][rr], ll = 0.f;
 #pragma unroll
     for (int k = 1; k < kWaves; ++k) top = fmaxf(top, s_m[k][rr]);
 #pragma unroll
     for (int k = 0; k < kWaves; ++k) ll += s_l[k][rr];
     const f32x4 sum = *reinterpret_cast<const f32x4*>(&s_o[0][rr][c]) + *reinterpret_cast<const f32x4*>(&s_o[1][rr][c]);
-    const int64_t token = tile.begin + at / group;
-    const int h = head * group + at % group;
+    const int64_t token = tile.begin + out_row / group;
+    const int h = head * group + out_row % group;
     const int64_t out = token * p.h_q + h;
     if (ns == 1) {
       const float inv = ll == 0.f ? 0.f : 1.f / ll;
       put<T>(p, sum * inv, token, (int64_t)h * D + c);
       if (p.lse && c == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (top + __log2f(ll)) * 0.69314718055994530942f;
     } else {
-      const int64_t part = (int64_t)piece * p.tokens * p.h_q + out;
+      const int64_t part = SHARES ? piece * kRows + rr : piece * p.tokens * p.h_q + out;
       *reinterpret_cast<f32x4*>(p.part_o + part * D + c) = sum;
       if (c == 0) p.part_ml[2 * part] = top, p.part_ml[2 * part + 1] = ll;
     }
+  }
+  if constexpr (SHARES) __syncthreads();  // the next tile's queries take the sums' place
   }
 }
 
@@ -814,19 +916,31 @@ __global__ __launch_bounds__(kWaves * 64, sizeof(T) == 4 && D == 256 ? 1 : 2) vo
 
 // Joins the pieces of a row: a wave a row, its lanes over the head's elements.  Lane s works out the factor of
 // piece s, and the pieces' rows are read several at a time.
-template <typename T, int D>
+template <typename T, int D, bool SHARES>
 __global__ __launch_bounds__(256) void join_kernel(AttendParams p) {
-  const int group = p.h_q / p.h_kv, lane = threadIdx.x & 63;
+  const int group = p.h_q / p.h_kv, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const Tile tile = find_tile(p, blockIdx.x, group, p.tile_rows);
   if (!tile.some) return;
-  const int ns = pieces(p, tile);
-  const int at = tile.first + blockIdx.z * 4 + (threadIdx.x >> 6);
+  const int at = tile.first + blockIdx.z * 4 + wave;
+  int ns;
+  int64_t part0 = 0;  // the first partial result's row
+  if constexpr (SHARES) {
+    const int64_t total = (int64_t)p.places[p.slots] * p.h_kv;
+    const int from = p.places[blockIdx.x], steps = p.places[blockIdx.x + 1] - from;
+    const int64_t begin = (int64_t)from * p.h_kv + (int64_t)blockIdx.y * steps;
+    const int first = share_of(p, total, begin);
+    ns = share_of(p, total, begin + steps - 1) - first + 1;
+    part0 = ((int64_t)blockIdx.x * p.h_kv + blockIdx.y + first) * kRows + (at - tile.first);
+  } else {
+    ns = pieces(p, tile);
+  }
   if (ns == 1 || at >= tile.rows) return;  // written already, or no row
   const int64_t token = tile.begin + at / group;
   const int h = blockIdx.y * group + at % group;
-  const int64_t out = token * p.h_q + h, step = p.tokens * p.h_q;
+  const int64_t out = token * p.h_q + h, step = SHARES ? kRows : p.tokens * p.h_q;
+  if (!SHARES) part0 = out;
   float mm = -__builtin_inff();
-  for (int s = lane; s < ns; s += 64) mm = fmaxf(mm, p.part_ml[2 * (s * step + out)]);
+  for (int s = lane; s < ns; s += 64) mm = fmaxf(mm, p.part_ml[2 * (s * step + part0)]);
 #pragma unroll
   for (int x = 32; x >= 1; x >>= 1) mm = fmaxf(mm, __shfl_xor(mm, x, 64));
   const float base = mm == -__builtin_inff() ? 0.f : mm;
@@ -837,14 +951,14 @@ __global__ __launch_bounds__(256) void join_kernel(AttendParams p) {
   for (int s0 = 0; s0 < ns; s0 += 64) {
     float a = 0.f;
     if (s0 + lane < ns) {
-      const int64_t part = (s0 + lane) * step + out;
+      const int64_t part = (s0 + lane) * step + part0;
       a = __builtin_amdgcn_exp2f(p.part_ml[2 * part] - base);
       ll += a * p.part_ml[2 * part + 1];
     }
     const int n = min(64, ns - s0);
     for (int s = 0; s < n; ++s) {
       const float as = __shfl(a, s, 64);
-      const float* row = p.part_o + ((s0 + s) * step + out) * D + lane * E;
+      const float* row = p.part_o + ((s0 + s) * step + part0) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) sum[e] = fmaf(as, row[e], sum[e]);
     }
@@ -870,6 +984,8 @@ struct Plan {
   int64_t uniform;
   int32_t piece;
   int64_t pieces;  // of the longest context that the table holds
+  int32_t shares;  // 0: pieces
+  int64_t parts;   // rows of partial results
 };
 
 // Tokens that a row of the page table holds; positions are 32-bit.
@@ -887,32 +1003,44 @@ Plan plan(const AttendShape& a) {
   c.tile_rows = !c.chunk ? kRows : kChunkRows;
   c.uniform_tiles = (int32_t)((c.uniform * group + c.tile_rows - 1) / c.tile_rows);
   c.slots = a.ragged ? a.tokens * group / c.tile_rows + a.n_seqs : (int64_t)c.uniform_tiles * a.n_seqs;
-  // Pieces: about 4096 workgroups where the contexts allow it (16 for each CU: unequal contexts then even
-  // out), of at least 256 tokens, a turn of a workgroup's four waves.  Chunks: about 1024 where there are
-  // fewer than 512 without pieces, of at least 512 tokens.
-  const int64_t most = max_tokens(a), step = c.chunk ? 512 : kWaves * kTok, tiles = c.slots * a.h_kv;
+  // Pieces of the contexts, for enough workgroups.  Single tokens: about 4096 (16 for each CU), of at least 256
+  // tokens, a turn of a workgroup's four waves.  Chunks: about 1024 where there are fewer than 512 without pieces,
+  // of at least 512 tokens.
+  const int64_t most = max_tokens(a), step = c.chunk ? 512 : kStep, tiles = c.slots * a.h_kv;
   int64_t piece = most;
   if (!c.chunk || tiles < 512) piece = (int64_t)std::min((double)most, (double)most * tiles / (c.chunk ? 1024 : 4096));
   piece = (piece + step - 1) / step * step;
-  if (const char* e = getenv(c.chunk ? "XPIECE" : "XPIECED")) piece = atoi(e);
   c.piece = (int32_t)(piece < step ? step : piece);
   c.pieces = (most + c.piece - 1) / c.piece;
   if (c.pieces < 1) c.pieces = 1;
+  // Shares instead, as many as run at once (2 workgroups to each of 256 CUs; 4 with heads of 64, 3 in fp32), where
+  // the longest contexts would give each at least 4 steps.
+  const int64_t at_once = 256 * (a.d != 64 ? 2 : a.bf16 ? 4 : 3);
+  c.shares = 0;
+  if (!c.chunk && !a.ragged && c.slots <= kMostTiles && tiles * ((most + kStep - 1) / kStep) >= 4 * at_once) c.shares = (int32_t)at_once;
+  c.parts = c.shares ? (c.shares + tiles) * kRows : c.pieces > 1 ? c.pieces * a.tokens * a.h_q : 0;
   return c;
 }
 
 template <typename T, int D>
-hipError_t launch(AttendParams p, const Plan& c, hipStream_t stream) {
-  const dim3 grid((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)c.pieces);
+hipError_t launch(const AttendParams& p, const Plan& c, hipStream_t stream) {
+  const dim3 block(kWaves * 64), joins((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)(c.tile_rows / 4));
+  if (c.shares) {
+    hipLaunchKernelGGL((attend_kernel<T, D, true>), dim3((unsigned)c.shares), block, 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((join_kernel<T, D, true>), joins, dim3(256), 0, stream, p);
+    return hipGetLastError();
+  }
   const int64_t turns = (c.slots * p.h_kv + 7) / 8;
-  const dim3 chunks((unsigned)(turns * 8), (unsigned)c.pieces);
-  if (c.chunk && p.page_shift >= 6) hipLaunchKernelGGL((attend_chunk_kernel<T, D, true>), chunks, dim3(kWaves * 64), 0, stream, p);
-  else if (c.chunk) hipLaunchKernelGGL((attend_chunk_kernel<T, D, false>), chunks, dim3(kWaves * 64), 0, stream, p);
-  else hipLaunchKernelGGL((attend_kernel<T, D>), grid, dim3(kWaves * 64), 0, stream, p);
-  hipError_t e = hipGetLastError();
+  if (turns > INT32_MAX / 8) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)c.pieces), chunks((unsigned)(turns * 8), (unsigned)c.pieces);
+  if (!c.chunk) hipLaunchKernelGGL((attend_kernel<T, D, false>), grid, block, 0, stream, p);
+  else if (p.page_shift >= 6) hipLaunchKernelGGL((attend_chunk_kernel<T, D, true>), chunks, block, 0, stream, p);
+  else hipLaunchKernelGGL((attend_chunk_kernel<T, D, false>), chunks, block, 0, stream, p);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || c.pieces == 1) return e;
-  hipLaunchKernelGGL((join_kernel<T, D>), dim3((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)(c.tile_rows / 4)), dim3(256), 0,
-                     stream, p);
+  hipLaunchKernelGGL((join_kernel<T, D, false>), joins, dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -932,9 +1060,8 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t attend_workspace_bytes(const AttendShape& a) {
   if (a.tokens == 0) return 0;
   const Plan c = plan(a);
-  if (c.pieces == 1) return 0;
-  const size_t rows = (size_t)c.pieces * a.tokens * a.h_q;
-  return round256(rows * a.d * sizeof(float)) + round256(rows * 2 * sizeof(float));
+  if (!c.parts) return 0;
+  return round256(c.parts * a.d * sizeof(float)) + round256(c.parts * 2 * sizeof(float)) + (c.shares ? round256((c.slots + 1) * sizeof(int)) : 0);
 }
 
 hipError_t launch_attend(AttendParams p, const AttendShape& a, void* workspace, int dtype, hipStream_t stream) {
@@ -946,10 +1073,13 @@ hipError_t launch_attend(AttendParams p, const AttendShape& a, void* workspace, 
   p.piece = c.piece;
   p.tile_rows = c.tile_rows;
   p.slots = (int32_t)c.slots;
-  if (c.pieces > 1) {
-    const size_t rows = (size_t)c.pieces * a.tokens * a.h_q;
-    p.part_o = reinterpret_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + round256(rows * a.d * sizeof(float)));
+  p.shares = c.shares;
+  if (c.parts) {
+    char* w = reinterpret_cast<char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(w);
+    w += round256(c.parts * a.d * sizeof(float));
+    p.part_ml = reinterpret_cast<float*>(w);
+    p.places = reinterpret_cast<int32_t*>(w + round256(c.parts * 2 * sizeof(float)));
   }
   return dtype == 1 ? launch_d<__bf16>(p, c, a.d, stream) : launch_d<float>(p, c, a.d, stream);
 }

@@ -295,8 +295,10 @@ struct AttendParams {
   int32_t piece;
   int32_t tile_rows;
   int32_t slots;
-  float* part_o;   // [pieces, tokens, h_q, d]
-  float* part_ml;  // [pieces, tokens, h_q, 2]
+  int32_t shares;
+  float* part_o;    // [pieces, tokens, h_q, d], or [shares + tiles, 16, d]
+  float* part_ml;   // a maximum and a sum for each of those rows
+  int32_t* places;  // [slots + 1] with shares
 };
 size_t attend_workspace_bytes(const AttendShape& a);
 hipError_t launch_attend(AttendParams p, const AttendShape& a, void* workspace, int dtype, hipStream_t stream);

@@ -329,3 +329,32 @@ def test_refusals():
                 dict(workspace=q), dict(out=q[:1]), dict(cache=gdn.kv_cache(4, 2, 64, 16)[:3]), dict(lens=ints([1])), dict(q=q.cpu())]:
         with pytest.raises(gdn.GdnError):
             gdn.cache_attention(**{**dict(q=q, cache=cache, page_table=table, lens=lens), **bad})
+
+
+SHARED = [
+    # contexts, new, h_q, h_kv, d, page, options: tables wide enough that the work is cut into shares
+    ([3000, 17, 0, 900], 1, 24, 4, 256, 64, {}),
+    ([500, 1200, 33, 64, 0, 2047], 1, 8, 8, 128, 16, dict(window=300)),
+    ([700, 90], 9, 16, 8, 64, 32, dict(gate=True)),
+    ([5000], 1, 6, 1, 256, 128, {}),
+    ([100] * 40, 1, 8, 2, 128, 256, {}),
+    ([4000, 5] * 3, 3, 1, 1, 64, 64, dict(causal=False)),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", range(len(SHARED)))
+def test_attention_in_shares(case, dtype):
+    """Contexts of unequal lengths under a table for far longer ones, pages outside the pool among them."""
+    ctx, new, h_q, h_kv, d, page, how = SHARED[case]
+    gen = torch.Generator().manual_seed(50 + case)
+    cache, table = filled(gen, ctx, h_kv, d, page, dtype, width=8192 * 64 // page // 16 * 4)
+    table[0, 1] = -1
+    how = dict(how)
+    q = torch.randn((len(ctx) * new, h_q, d), generator=gen).to(dtype).cuda()
+    if how.pop("gate", False):
+        how["gate"] = torch.randn(q.shape, generator=gen).to(dtype).cuda()
+    got = gdn.cache_attention(q, cache, table, ints(ctx), return_lse=True, **how)
+    ref.close_attention(got, ref.cache_attention(q, cache, table, ints(ctx), **how), f"shares {case}")
+    again = gdn.cache_attention(q, cache, table, ints(ctx), return_lse=True, **how)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
