@@ -37,6 +37,7 @@
 // pieces by their maxima and sums, in order.
 #include "gdn_device.h"
 #include "gdn_internal.h"
+#include "sequences.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -674,10 +675,10 @@ __global__ __launch_bounds__(kWaves * 64, sizeof(T) == 4 && D == 256 ? 1 : 2) vo
   for (int i = 0; i < MT; ++i) o[i] = zeros16();
   float m = -__builtin_inff(), l = 0.f;
 
-  // what all of this wave's rows see, and what any of them does
-  const bool live_row = row_hi > 0;
+  // what all of this wave's rows see (nothing, where one of them has no keys), and what any of them does
+  const bool live_row = tile.first + wave * 32 + c < tile.rows;
   const int all_lo = wave_max(live_row ? row_lo : 0), all_hi = wave_min(live_row ? row_hi : INT32_MAX);
-  const int any_lo = wave_min(live_row ? row_lo : INT32_MAX), any_hi = wave_max(row_hi);
+  const int any_lo = wave_min(live_row && row_hi > 0 ? row_lo : INT32_MAX), any_hi = wave_max(row_hi);
 
   const int start = tile.lo + piece * p.piece;
   const int stop = min(tile.hi, start + p.piece);

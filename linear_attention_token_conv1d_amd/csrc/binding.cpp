@@ -6,11 +6,13 @@
 //
 // Every function takes the positional arguments of its namesake in block.py
 // and raises GdnError (given to init) as the rest of the package does.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 
+#include <cmath>
 #include <string>
 
 #include "../../include/gdn.h"
@@ -390,22 +392,20 @@ PyObject* cache_attention(PyObject* const* a) {
   return want_lse ? tuple({o, lse}) : wrap(o);
 }
 
-// No C++ exception leaves a call.
+// No C++ exception leaves a call: torch's (out of memory, say) become its Python ones.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
     PyErr_Format(PyExc_TypeError, "%zd arguments expected, got %zd", N, n);
     return nullptr;
   }
+  HANDLE_TH_ERRORS
   try {
     return F(args);
   } catch (const Raised&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "internal error");
+    return nullptr;
   }
-  return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 // (GdnError, stream of a device, current device, set the current device)

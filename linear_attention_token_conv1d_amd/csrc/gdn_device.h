@@ -173,22 +173,4 @@ __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.0f + __e
 typedef const __attribute__((address_space(4))) int32_t cint32;
 __device__ __forceinline__ cint32* as_const(const int32_t* p) { return (cint32*)p; }
 
-// The last n in [0, n_seqs) with key(cu[n], n) <= slot, where keys rise and
-// key(cu[0], 0) <= slot: which sequence a workgroup's slot belongs to.  A wave
-// compares 64 sequences at a time (one trip to memory for a pack of up to 64,
-// where a binary search takes six, one after another).  Every lane of the wave
-// takes part; the result is uniform.
-template <typename F>
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int n_seqs, int64_t slot, F&& key) {
-  int count = 0;
-  for (int base = 0; base < n_seqs; base += 64) {
-    const int n = base + (int)(threadIdx.x & 63);
-    const bool at_most = n < n_seqs && key((int64_t)cu[n], n) <= slot;
-    const int got = (int)__popcll(__ballot(at_most));
-    count += got;
-    if (got < 64) break;
-  }
-  return __builtin_amdgcn_readfirstlane(max(count - 1, 0));
-}
-
 }  // namespace gdn

@@ -17,6 +17,7 @@
 // its matrix products take them.  Values are turned round through LDS.
 #include "gdn_device.h"
 #include "gdn_internal.h"
+#include "sequences.h"
 
 namespace gdn {
 namespace {

@@ -203,7 +203,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p
     }
     group_sum<G>(sums);
     const float r = 1.0f / sqrtf(sums[0] * inv_width + p.eps);
-    const float c = post * r * r * r * (sums[1] * inv_width);  // dh = r u - c h:  r mean(u n) n = r^3 mean(u h) h
+    const float mean = post * r * (sums[1] * inv_width);  // of u n
     if (row >= p.rows) return;
     uint32_t t;
     int64_t col;
@@ -215,15 +215,15 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p
       float dx[VEC], dz[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float h = to_f32(d.x[v].v[e]), dyr = post * r * to_f32(d.g[v].v[e]), wt = w[v].get(p.weight, p.weight_offset, e);
+        const float n = to_f32(d.x[v].v[e]) * r, dy = post * to_f32(d.g[v].v[e]), wt = w[v].get(p.weight, p.weight_offset, e);
         float a = 1.f;
-        const float nd = dyr * h;  // dy n
+        const float nd = dy * n;
         if (p.gate) {
           const float z = to_f32(d.z[v].v[e]), sg = s[v][e];
           a = p.act == 1 ? z * sg : sg;
           dz[e] = nd * wt * (p.act == 1 ? sg * (1.f + z * (1.f - sg)) : sg * (1.f - sg));
         }
-        dx[e] = fmaf(-c, h, dyr * wt * a);
+        dx[e] = r * fmaf(-n, mean, dy * wt * a);
         if (p.d_sum) dx[e] += to_f32(d.ds[v].v[e]);
         dw[v][e] = fmaf(nd, a, dw[v][e]);
       }

@@ -358,3 +358,107 @@ def test_attention_in_shares(case, dtype):
     ref.close_attention(got, ref.cache_attention(q, cache, table, ints(ctx), **how), f"shares {case}")
     again = gdn.cache_attention(q, cache, table, ints(ctx), return_lse=True, **how)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+CHUNKS = [
+    # new, contexts, h_q, h_kv, d, page, options: rows enough to share a workgroup's tiles
+    ([200], [100], 4, 2, 64, 64, {}),                      # rows whose position lies before the first token
+    ([100, 37], [60, 37], 40, 1, 128, 32, {}),             # 40 heads to one, empty rows among them
+    ([300], [301], 3, 3, 128, 64, dict(gate=True)),        # heads that do not divide the XCDs
+    ([64, 64], [64, 700], 16, 16, 64, 16, {}),
+    ([130], [1500], 8, 2, 256, 128, dict(window=1)),
+    ([130], [1500], 8, 2, 128, 16, dict(window=700, gate=True)),
+    ([90, 80], [500, 80], 8, 2, 256, 32, dict(causal=False, window=90)),
+    ([513], [1024], 2, 1, 64, 256, dict(scale=0.7)),
+    ([1000], [1000], 6, 1, 128, 64, {}),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", range(len(CHUNKS)))
+def test_chunks(case, dtype):
+    """Chunks of prompts: strided queries, gates and outputs, every page size, contexts cut into pieces."""
+    new, ctx, h_q, h_kv, d, page, how = CHUNKS[case]
+    gen = torch.Generator().manual_seed(70 + case)
+    cache, table = filled(gen, ctx, h_kv, d, page, dtype, scales="any")
+    how, T = dict(how), sum(new)
+
+    def strided():
+        return torch.randn((T, h_q * d + 24), generator=gen).to(dtype).cuda()[:, 8:8 + h_q * d].unflatten(1, (h_q, d))
+
+    q = strided()
+    if how.pop("gate", False):
+        how["gate"] = strided()
+    out = torch.full((T + 2, h_q, d + 0), 7.0, dtype=dtype, device="cuda")
+    cu = cu_of(new)
+    got = gdn.cache_attention(q, cache, table, ints(ctx), cu, out=out[:T], return_lse=True, **how)
+    assert got[0].data_ptr() == out.data_ptr() and torch.all(out[T:] == 7.0)
+    ref.close_attention(got, ref.cache_attention(q, cache, table, ints(ctx), cu, **how), f"chunk {case}")
+
+
+def test_nan_in_a_chunk():
+    """A NaN among the values of a chunk's own tokens reaches the rows from that token on, and a page that two tiles of
+    rows share is not changed for the next."""
+    gen = torch.Generator().manual_seed(80)
+    d, page, T, heads = 64, 64, 300, 2
+    cache, table = filled(gen, [T], heads, d, page)
+    q = torch.randn((T, 4, d), generator=gen).to(BF16).cuda()
+    clean = gdn.cache_attention(q, cache, table, ints([T]))
+    bad = [t.clone() for t in cache]
+    spots = [(10, 0, 5), (100, 1, 63), (101, 1, 0), (299, 0, 33)]
+    for at, head, c in spots:
+        bad[1].view(torch.uint8)[int(table[0, at // page]), head, c, at % page] = NAN
+    o = gdn.cache_attention(q, bad, table, ints([T]))
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    for at, head, c in spots:
+        hit[at:, 2 * head:2 * head + 2, c] = True
+    assert torch.equal(torch.isnan(o), hit) and torch.equal(o[~hit], clean[~hit])
+
+
+def test_many_sequences():
+    """More sequences than a wave looks at at once, most of them with no or few new tokens."""
+    gen = torch.Generator().manual_seed(81)
+    n, page, d = 300, 16, 64
+    new = torch.randint(0, 4, (n,), generator=gen).tolist()
+    new[7], new[150], new[299] = 40, 0, 9
+    old = torch.randint(0, 50, (n,), generator=gen).tolist()
+    total = [a + b for a, b in zip(new, old)]
+    table, pages = tables(gen, total, page)
+    cache = pool(pages, 1, d, page)
+    k = rand(gen, sum(old), 1, d, BF16)
+    check_store(k, -k, cache, table, ints([0] * n), cu_of(old), "old")
+    k = rand(gen, sum(new) + 5, 1, d, BF16, scale=4.0)  # a padded batch
+    check_store(k, k, cache, table, ints(old), cu_of(new), "new")
+    q = torch.randn((sum(new), 2, d), generator=gen).to(BF16).cuda()
+    got = gdn.cache_attention(q, cache, table, ints(total), cu_of(new), return_lse=True)
+    ref.close_attention(got, ref.cache_attention(q, cache, table, ints(total), cu_of(new)), "many")
+
+
+def test_offsets_beyond_32_bits():
+    """Pages of a pool beyond 4 GiB of codes."""
+    gen = torch.Generator().manual_seed(82)
+    heads, d, page, pages = 4, 256, 64, 66000
+    assert pages * heads * d * page > 1 << 32
+    big = gdn.KVCache(torch.empty((pages, heads, page, d), dtype=torch.uint8, device="cuda").view(FP8),
+                      torch.empty((pages, heads, d, page), dtype=torch.uint8, device="cuda").view(FP8),
+                      torch.empty((pages, heads), device="cuda"), torch.empty((pages, heads), device="cuda"))
+    small = pool(4, heads, d, page)
+    far = ints([[pages - 1, pages - 3], [pages - 2, 65537]])
+    near = ints([[0, 1], [2, 3]])
+    for new in (1, 100):
+        T = 2 * new
+        k, v = rand(gen, T, heads, d, BF16), rand(gen, T, heads, d, BF16)
+        held = [0, 0] if new == 100 else [100, 100]
+        q = torch.randn((T, 24, d), generator=gen).to(BF16).cuda()
+        for c, t in ((big, far), (small, near)):
+            if new == 1:
+                gdn.cache_store(k.repeat(100, 1, 1), v.repeat(100, 1, 1), c, t, ints([0, 0]))
+            gdn.cache_store(k, v, c, t, ints(held))
+        lens = ints([h + new for h in held])
+        assert torch.equal(gdn.cache_attention(q, big, far, lens), gdn.cache_attention(q, small, near, lens))
+        for n in range(2):
+            for j in range(2):
+                a, b = int(far[n, j]), int(near[n, j])
+                tokens = min(max(int(lens[n]) - j * page, 0), page)
+                assert torch.equal(big.k[a].view(torch.uint8)[:, :tokens], small.k[b].view(torch.uint8)[:, :tokens])
+                assert torch.equal(big.v[a].view(torch.uint8)[..., :tokens], small.v[b].view(torch.uint8)[..., :tokens])

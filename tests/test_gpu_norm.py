@@ -204,3 +204,26 @@ def test_refusals():
         gdn.rms_norm_backward(x, x, order="post", residual=True)
     with pytest.raises(gdn.GdnError):
         gdn.rms_norm_backward(x, x, scale=0.5)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows behind the first 2^31 elements."""
+    T, D = 270000, 8192
+    x = torch.empty((T, D), dtype=BF16, device="cuda")
+    tail = torch.randn((5, D), generator=torch.Generator().manual_seed(9)).to(BF16).cuda()
+    x[-5:] = tail
+    w = torch.ones(D, dtype=BF16, device="cuda")
+    y = gdn.rms_norm(x, w)
+    assert torch.equal(y[-5:], gdn.rms_norm(tail, w))
+    dx = gdn.rms_norm_backward(x, x, w, dx=y)[0]
+    assert torch.equal(dx[-5:], gdn.rms_norm_backward(tail, tail, w)[0])
+
+
+def test_small_rows_without_eps():
+    """The gradient of rows so small that the third power of 1 / rms is beyond fp32."""
+    gen = torch.Generator().manual_seed(10)
+    x = 1e-14 * torch.randn((4, 1, 256), generator=gen).cuda()
+    dy = torch.randn((4, 1, 256), generator=gen).cuda()
+    dx = gdn.rms_norm_backward(x, dy, eps=0.0)[0]
+    rh, sh, *_ = ref.rms_norm_backward(x, dy, None, None, None, "pre", "silu", 1.0, 0.0, 0.0)
+    ref.close(dx, rh, sh, 64, "dx")

@@ -105,3 +105,15 @@ def test_refusals():
                      ((q, pos, inv), dict(mscale=float("inf"))), ((q[:, 0], pos, inv), {})]:
         with pytest.raises(gdn.GdnError):
             gdn.rope(*args, **kw)
+
+
+def test_offsets_beyond_32_bits():
+    """Tokens behind the first 2^31 elements, and more threads than 32 bits count where pairs are single."""
+    T, H, d = 2100000, 8, 130
+    q = torch.empty((T, H, d), dtype=BF16, device="cuda")
+    tail = torch.randn((7, H, d), generator=torch.Generator().manual_seed(9)).to(BF16).cuda()
+    q[-7:] = tail
+    inv, _ = gdn.rope_frequencies(64, device="cuda")
+    pos = torch.arange(T, device="cuda")
+    gdn.rope(q, pos, inv, out=q)
+    assert torch.equal(q[-7:], gdn.rope(tail, pos[-7:], inv))
