@@ -704,8 +704,9 @@ gdn_status gdn_cache_store(const gdn_cache_store_args* args, void* stream);
  *   workspace    gdn_cache_attention_workspace_size() bytes, 256-byte aligned:
  *                partial results of long contexts cut into pieces.
  *   The cache and its table as in gdn_cache_store (scales of any positive
- *   value, e4m3 codes written by others too); a page outside the pool holds no
- *   tokens.  tokens * h_q / h_kv < 2^31.
+ *   value, e4m3 codes written by others too; bf16 outputs have fewer bits from
+ *   pages whose value scale lies below 2^-100); a page outside the pool holds
+ *   no tokens.  tokens * h_q / h_kv <= 2^30.
  * NaN and infinities in keys or values that a token does not see do not
  * reach it.
  * ---------------------------------------------------------------------- */

@@ -132,19 +132,27 @@ struct Tile {
   bool some;       // whether there is such a tile
 };
 
+// The keys that the tile's sequence's new token i sees: from keys_from to keys_to - 1, both in [0, ctx].  (Neither a
+// position before the first key nor a window of 2^31 - 1 may pass 32 bits.)
+__device__ __forceinline__ int keys_to(const AttendParams& p, const Tile& t, int i) {
+  return p.causal ? max(0, min(t.ctx, t.ctx - t.len + i + 1)) : t.ctx;
+}
+__device__ __forceinline__ int keys_from(const AttendParams& p, const Tile& t, int i) {
+  return p.window ? min(t.ctx, max(0, max(0, t.ctx - t.len + i) - p.window + 1)) : 0;
+}
+
 // Tile j of a sequence whose number, first token, length and context are known.
 __device__ __forceinline__ Tile finish_tile(const AttendParams& p, Tile t, int j, int group, int tile_rows) {
   t.rows = t.len * group;
   t.first = j * tile_rows;
   t.some = t.len > 0 && j >= 0 && t.first < t.rows;
-  t.ctx = min(t.ctx, p.max_tokens);  // contexts end with the table
+  t.ctx = max(0, min(t.ctx, p.max_tokens));  // contexts end with the table
   if (!t.some) return t;
   const int t0 = t.first / group, t1 = min(t.len - 1, (t.first + tile_rows - 1) / group);
-  t.hi = p.causal ? min(t.ctx, t.ctx - t.len + t1 + 1) : t.ctx;
-  t.all_hi = p.causal ? min(t.ctx, t.ctx - t.len + t0 + 1) : t.ctx;
-  t.all_lo = p.window ? t.ctx - t.len + t1 - p.window + 1 : 0;
-  t.lo = p.window ? max(0, t.ctx - t.len + t0 - p.window + 1) : 0;
-  t.lo &= ~(kTok - 1);
+  t.hi = keys_to(p, t, t1);
+  t.all_hi = keys_to(p, t, t0);
+  t.all_lo = keys_from(p, t, t1);
+  t.lo = keys_from(p, t, t0) & ~(kTok - 1);
   if (t.hi < t.lo) t.hi = t.lo;
   return t;
 }
@@ -214,6 +222,20 @@ __device__ __forceinline__ void put(const AttendParams& p, f32x4 o, int64_t toke
     for (int e = 0; e < 4; ++e) y[e] = gated<T>(y[e], z[e]);
   }
   store4(reinterpret_cast<T*>(p.o) + token * p.o_stride + at, y);
+}
+
+// The running maximum is that of score + log2 vscale, so that the weights, 2^(score - max) vscale, fit 16 bits; the
+// sum of 2^(score - max) then ranges from 2^-120 to 2^98 with the scales.  The exponential gives no subnormals: it
+// is taken 2^28 times as large, which brings terms of the smallest sum into its range and leaves the largest in it.
+// A scale counts as 2^-90 at least: pages of zeros have the least there is.
+constexpr float kUp = 28.f, kDown = 0x1p-28f;
+__device__ __forceinline__ float log2_scale(float vs) { return fmaxf(__log2f(fabsf(vs)), -90.f); }
+// From one maximum to a larger one: a sum l 2^x, where 2^x alone may be below fp32 (a page's sum is as large as its
+// scale is small), and 2^x for the outputs.
+__device__ __forceinline__ float lower(float& l, float x) {
+  const float half = __builtin_amdgcn_exp2f(0.5f * x);
+  l = l * half * half;
+  return half * half;
 }
 
 // 16 bytes that no other workgroup reads soon: nontemporal (a decode step of 64 sequences of up to 32768 tokens 386 ->
@@ -308,253 +330,250 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
       for (int i = threadIdx.x; i <= p.slots; i += kWaves * 64) p.places[i] = s_place[i];
   }
   while (at < end) {
-  int head = blockIdx.y, ns, start, stop;
-  int64_t piece = blockIdx.z;  // which partial result this is
-  Tile tile;
-  if constexpr (SHARES) {
-    int lo = 0, hi = p.slots - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)s_place[mid] * p.h_kv <= at) lo = mid; else hi = mid - 1;
-    }
-    const int slot = __builtin_amdgcn_readfirstlane(lo);
-    const int steps = __builtin_amdgcn_readfirstlane(s_place[slot + 1] - s_place[slot]);
-    const int64_t rest = at - (int64_t)__builtin_amdgcn_readfirstlane(s_place[slot]) * p.h_kv;
-    head = (int)(rest / steps);
-    const int step = (int)(rest - (int64_t)head * steps), n = (int)min((int64_t)(steps - step), end - at);
-    tile = find_tile(p, slot, group, kRows);
-    start = tile.lo + step * kStep;
-    stop = min(tile.hi, start + n * kStep);
-    ns = n == steps ? 1 : 2;  // the whole tile, or a part of it
-    piece = (int64_t)slot * p.h_kv + head + blockIdx.x;
-    at += n;
-  } else {
-    at = end;
-    // workgroups go to the 8 XCDs in turn: every XCD gets pieces of every sequence, however unequal those are
-    tile = find_tile(p, (blockIdx.x + blockIdx.z) % gridDim.x, group, kRows);
-    if (!tile.some) return;
-    ns = pieces(p, tile);
-    if (piece >= ns) return;
-    start = tile.lo + (int)piece * p.piece;
-    stop = min(tile.hi, start + p.piece);
-  }
-
-  // A wave's codes stay on their way: a tile's keys are asked for when the last tile's have been used, and so
-  // are its values; its pages a tile before that.
-  const int32_t* table = p.page_table + (int64_t)tile.n * p.max_pages;
-  // pages of this lane's 16 tokens as a row of the keys, and as a column of the scores
-  auto page_of = [&](int token) { return token < stop ? table[token >> p.page_shift] : -1; };
-  uint4 kc[4][D / 64], vc[MT];
-  auto load_keys = [&](int k0, int pk) {
-    const uint8_t* kp = p.k_cache + ((((int64_t)inside(pk) * p.h_kv + head) << p.page_shift) + ((k0 + 16 * kg) & in_page) + ki) * D + g * 16;
-#pragma unroll
-    for (int b = 0; b < D / 64; ++b)
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) kc[tt][b] = load_codes<!F32>(kp + tt * 4 * D + b * 64);
-  };
-  auto load_values = [&](int k0, int ps) {
-    const uint8_t* vp = p.v_cache + ((((int64_t)inside(ps) * p.h_kv + head) * D + r) << p.page_shift) + ((k0 + 16 * g) & in_page);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) vc[i] = load_codes<!F32>(vp + ((i * 16) << p.page_shift));
-  };
-  const int k_first = start + wave * kTok;
-  int pk = page_of(k_first + 16 * kg), ps = page_of(k_first + 16 * g);
-  int pk_next = page_of(k_first + kStep + 16 * kg), ps_next = page_of(k_first + kStep + 16 * g);
-  float ks = 0.f, vs = 0.f;
-  if (k_first < stop) {
-    load_keys(k_first, pk);
-    load_values(k_first, ps);
-    ks = p.k_scale[(int64_t)inside(ps) * p.h_kv + head], vs = p.v_scale[(int64_t)inside(ps) * p.h_kv + head];
-  }
-
-  // this lane's row
-  const int row = tile.first + r;
-  const bool live = row < tile.rows;  // the last tile's other rows see nothing and are not written
-  const int tok = row / group, hq = head * group + (row - tok * group);
-  const int pos = tile.ctx - tile.len + tok;
-  const int row_hi = live ? (p.causal ? min(tile.ctx, pos + 1) : tile.ctx) : 0;
-  const int row_lo = p.window ? pos - p.window + 1 : 0;
-
-  // Q: lane (row r, group g) holds elements 64 b + 16 g .. + 15 of each 64, the order its keys come in.  The
-  // four waves make the operands together.
-#pragma unroll
-  for (int k = wave; k < KS; k += kWaves) {
-    const int at = (k / 2) * 64 + g * 16 + (k & 1) * 8;
-    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live) load8(reinterpret_cast<const T*>(p.q) + (tile.begin + tok) * p.q_stride + (int64_t)hq * D + at, f);
-    bf16x8 q[NQ];
-    if constexpr (F32) {
-      split3_any(f, q);
+    int head = blockIdx.y, ns, start, stop;
+    int64_t piece = blockIdx.z;  // which partial result this is
+    Tile tile;
+    if constexpr (SHARES) {
+      int lo = 0, hi = p.slots - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)s_place[mid] * p.h_kv <= at) lo = mid; else hi = mid - 1;
+      }
+      const int slot = __builtin_amdgcn_readfirstlane(lo);
+      const int steps = __builtin_amdgcn_readfirstlane(s_place[slot + 1] - s_place[slot]);
+      const int64_t rest = at - (int64_t)__builtin_amdgcn_readfirstlane(s_place[slot]) * p.h_kv;
+      head = (int)(rest / steps);
+      const int step = (int)(rest - (int64_t)head * steps), n = (int)min((int64_t)(steps - step), end - at);
+      tile = find_tile(p, slot, group, kRows);
+      start = tile.lo + step * kStep;
+      stop = min(tile.hi, start + n * kStep);
+      ns = n == steps ? 1 : 2;  // the whole tile, or a part of it
+      piece = (int64_t)slot * p.h_kv + head + blockIdx.x;
+      at += n;
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[0][i] = (__bf16)f[i];
+      at = end;
+      // workgroups go to the 8 XCDs in turn: every XCD gets pieces of every sequence, however unequal those are
+      tile = find_tile(p, (blockIdx.x + blockIdx.z) % gridDim.x, group, kRows);
+      if (!tile.some) return;
+      ns = pieces(p, tile);
+      if (piece >= ns) return;
+      start = tile.lo + (int)piece * p.piece;
+      stop = min(tile.hi, start + p.piece);
     }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) s_q[(k * NQ + i) * 64 + lane] = q[i];
-  }
-  __syncthreads();
 
-  f32x4 o[MT];
+    // A wave's codes stay on their way: a tile's keys are asked for when the last tile's have been used, and so
+    // are its values; its pages a tile before that.
+    const int32_t* table = p.page_table + (int64_t)tile.n * p.max_pages;
+    // pages of this lane's 16 tokens as a row of the keys, and as a column of the scores
+    auto page_of = [&](int token) { return token < stop ? table[token >> p.page_shift] : -1; };
+    uint4 kc[4][D / 64], vc[MT];
+    auto load_keys = [&](int k0, int pk) {
+      const uint8_t* kp = p.k_cache + ((((int64_t)inside(pk) * p.h_kv + head) << p.page_shift) + ((k0 + 16 * kg) & in_page) + ki) * D + g * 16;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -__builtin_inff(), l = 0.f;
+      for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) kc[tt][b] = load_codes<!F32>(kp + tt * 4 * D + b * 64);
+    };
+    auto load_values = [&](int k0, int ps) {
+      const uint8_t* vp = p.v_cache + ((((int64_t)inside(ps) * p.h_kv + head) * D + r) << p.page_shift) + ((k0 + 16 * g) & in_page);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) vc[i] = load_codes<!F32>(vp + ((i * 16) << p.page_shift));
+    };
+    const int k_first = start + wave * kTok;
+    int pk = page_of(k_first + 16 * kg), ps = page_of(k_first + 16 * g);
+    int pk_next = page_of(k_first + kStep + 16 * kg), ps_next = page_of(k_first + kStep + 16 * g);
+    float ks = 0.f, vs = 0.f;
+    if (k_first < stop) {
+      load_keys(k_first, pk);
+      load_values(k_first, ps);
+      ks = p.k_scale[(int64_t)inside(ps) * p.h_kv + head], vs = p.v_scale[(int64_t)inside(ps) * p.h_kv + head];
+    }
+
+    // this lane's row
+    const int row = tile.first + r;
+    const bool live = row < tile.rows;  // the last tile's other rows see nothing and are not written
+    const int tok = row / group, hq = head * group + (row - tok * group);
+    const int row_hi = live ? keys_to(p, tile, tok) : 0, row_lo = keys_from(p, tile, tok);
+
+    // Q: lane (row r, group g) holds elements 64 b + 16 g .. + 15 of each 64, the order its keys come in.  The
+    // four waves make the operands together.
+#pragma unroll
+    for (int k = wave; k < KS; k += kWaves) {
+      const int at = (k / 2) * 64 + g * 16 + (k & 1) * 8;
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (live) load8(reinterpret_cast<const T*>(p.q) + (tile.begin + tok) * p.q_stride + (int64_t)hq * D + at, f);
+      bf16x8 q[NQ];
+      if constexpr (F32) {
+        split3_any(f, q);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[0][i] = (__bf16)f[i];
+      }
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) s_q[(k * NQ + i) * 64 + lane] = q[i];
+    }
+    __syncthreads();
+
+    f32x4 o[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -__builtin_inff(), l = 0.f;
 
 #pragma unroll 1
-  for (int k0 = k_first; k0 < stop; k0 += kStep) {
-    const int ts = k0 + 16 * g;
-    const bool held = ps >= 0 && ps < p.pages;  // a page outside the pool holds nothing
-    const bool more = k0 + kStep < stop;
-    float ks_next = 0.f, vs_next = 0.f;
-    if (more) ks_next = p.k_scale[(int64_t)inside(ps_next) * p.h_kv + head], vs_next = p.v_scale[(int64_t)inside(ps_next) * p.h_kv + head];
+    for (int k0 = k_first; k0 < stop; k0 += kStep) {
+      const int ts = k0 + 16 * g;
+      const bool held = ps >= 0 && ps < p.pages;  // a page outside the pool holds nothing
+      const bool more = k0 + kStep < stop;
+      float ks_next = 0.f, vs_next = 0.f;
+      if (more) ks_next = p.k_scale[(int64_t)inside(ps_next) * p.h_kv + head], vs_next = p.v_scale[(int64_t)inside(ps_next) * p.h_kv + head];
 
-    f32x4 s[4];
+      f32x4 s[4];
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) s[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int tt = 0; tt < 4; ++tt) s[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int b = 0; b < D / 64; ++b) {
-      bf16x8 q[2][NQ];
+      for (int b = 0; b < D / 64; ++b) {
+        bf16x8 q[2][NQ];
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) q[0][i] = s_q[(2 * b * NQ + i) * 64 + lane], q[1][i] = s_q[((2 * b + 1) * NQ + i) * 64 + lane];
+        for (int i = 0; i < NQ; ++i) q[0][i] = s_q[(2 * b * NQ + i) * 64 + lane], q[1][i] = s_q[((2 * b + 1) * NQ + i) * 64 + lane];
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const bf16x8 k_lo = to_bf16x8(kc[tt][b].x, kc[tt][b].y), k_hi = to_bf16x8(kc[tt][b].z, kc[tt][b].w);
+        for (int tt = 0; tt < 4; ++tt) {
+          const bf16x8 k_lo = to_bf16x8(kc[tt][b].x, kc[tt][b].y), k_hi = to_bf16x8(kc[tt][b].z, kc[tt][b].w);
 #pragma unroll
-        for (int i = NQ - 1; i >= 0; --i) {
-          s[tt] = mfma(k_lo, q[0][i], s[tt]);
-          s[tt] = mfma(k_hi, q[1][i], s[tt]);
+          for (int i = NQ - 1; i >= 0; --i) {
+            s[tt] = mfma(k_lo, q[0][i], s[tt]);
+            s[tt] = mfma(k_hi, q[1][i], s[tt]);
+          }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if (more) load_keys(k0 + kStep, pk_next);
       __builtin_amdgcn_sched_barrier(0);
-    }
-    if (more) load_keys(k0 + kStep, pk_next);
-    __builtin_amdgcn_sched_barrier(0);
 
-    // this lane's row against tokens ts .. ts + 15 (s[tt][i]: token ts + 4 tt + i): it sees from .. to - 1 of them
-    const float f = ks * p.scale_log2;
-    const int from = max(0, min(row_lo - ts, 16)), to = held ? max(0, min(row_hi - ts, 16)) : 0;
-    const bool sees = from < to;
-    const bool part = __any(live && (from > 0 || to < 16));  // some row sees some of the tile only
-    if (part) {
+      // this lane's row against tokens ts .. ts + 15 (s[tt][i]: token ts + 4 tt + i): it sees from .. to - 1 of them
+      const float f = ks * p.scale_log2;
+      const int from = max(0, min(row_lo - ts, 16)), to = held ? max(0, min(row_hi - ts, 16)) : 0;
+      const bool sees = from < to;
+      const bool part = __any(live && (from > 0 || to < 16));  // some row sees some of the tile only
+      if (part) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (e < from || e >= to) s[e >> 2][e & 3] = -__builtin_inff();
-    }
-    float top = s[0][0];
+        for (int e = 0; e < 16; ++e)
+          if (e < from || e >= to) s[e >> 2][e & 3] = -__builtin_inff();
+      }
+      float top = s[0][0];
 #pragma unroll
-    for (int e = 1; e < 15; e += 2) top = max3(top, s[e >> 2][e & 3], s[(e + 1) >> 2][(e + 1) & 3]);
-    top = fmaxf(top, s[3][3]);
-    // (the scales are positive, so the largest product is that of the largest score)
-    top = sees ? fmaf(top, f, fminf(fmaxf(__log2f(fabsf(vs)), -40.f), 120.f)) : -__builtin_inff();
-    top = group_max(top);
-    // the maximum moves only where it grows by more than 2^8: the weights then stay under 256
-    if (__any(top > m + 8.f)) {
-      const float now = fmaxf(m, top);
-      const float alpha = now == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - now);
-      m = now;
-      l *= alpha;
+      for (int e = 1; e < 15; e += 2) top = max3(top, s[e >> 2][e & 3], s[(e + 1) >> 2][(e + 1) & 3]);
+      top = fmaxf(top, s[3][3]);
+      // (the scales are positive, so the largest product is that of the largest score)
+      top = sees ? fmaf(top, f, log2_scale(vs)) : -__builtin_inff();
+      top = group_max(top);
+      // the maximum moves only where it grows by more than 2^8: the weights then stay under 256
+      if (__any(top > m + 8.f)) {
+        const float now = fmaxf(m, top);
+        const float alpha = lower(l, now == -__builtin_inff() ? now : m - now);
+        m = now;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) o[i] *= alpha;
-    }
-    const float base = m == -__builtin_inff() ? 0.f : m;
-    float w[2][8];
+        for (int i = 0; i < MT; ++i) o[i] *= alpha;
+      }
+      const float base = (m == -__builtin_inff() ? 0.f : m) - kUp;
+      float w[2][8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) w[e >> 3][e & 7] = __builtin_amdgcn_exp2f(fmaf(s[e >> 2][e & 3], f, -base));
-    if (part) {
+      for (int e = 0; e < 16; ++e) w[e >> 3][e & 7] = __builtin_amdgcn_exp2f(fmaf(s[e >> 2][e & 3], f, -base));
+      if (part) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (e < from || e >= to) w[e >> 3][e & 7] = 0.f;
-    }
-    const float factor = sees ? vs : 0.f;  // whatever stands where no page is
+        for (int e = 0; e < 16; ++e)
+          if (e < from || e >= to) w[e >> 3][e & 7] = 0.f;
+      }
+      const float factor = sees ? vs * kDown : 0.f;  // whatever stands where no page is
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      l += w[e >> 3][e & 7];
-      w[e >> 3][e & 7] *= factor;
-    }
+      for (int e = 0; e < 16; ++e) {
+        l = fmaf(w[e >> 3][e & 7], kDown, l);
+        w[e >> 3][e & 7] *= factor;
+      }
 
-    if (part) {
-      // codes that must not reach the product: tokens behind the context or of no page, and NaN
-      const int n = held ? tile.ctx - ts : 0;
-      const uint2 keep[2] = {first_codes(n), first_codes(n - 8)};
+      if (part) {
+        // codes that must not reach the product: tokens behind the context or of no page, and NaN
+        const int n = held ? tile.ctx - ts : 0;
+        const uint2 keep[2] = {first_codes(n), first_codes(n - 8)};
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        uint32_t* c = reinterpret_cast<uint32_t*>(&vc[i]);
+        for (int i = 0; i < MT; ++i) {
+          uint32_t* c = reinterpret_cast<uint32_t*>(&vc[i]);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          c[2 * u] &= keep[u].x, c[2 * u + 1] &= keep[u].y;
-          const uint2 bad = make_uint2(nan_bytes(c[2 * u]), nan_bytes(c[2 * u + 1]));
-          if (__any((bad.x | bad.y) != 0)) {
-            give_nan<T>(bad, from - 8 * u, to - 8 * u, o[i]);
-            c[2 * u] &= ~(bad.x * 0xffu), c[2 * u + 1] &= ~(bad.y * 0xffu);
+          for (int u = 0; u < 2; ++u) {
+            c[2 * u] &= keep[u].x, c[2 * u + 1] &= keep[u].y;
+            const uint2 bad = make_uint2(nan_bytes(c[2 * u]), nan_bytes(c[2 * u + 1]));
+            if (__any((bad.x | bad.y) != 0)) {
+              give_nan<T>(bad, from - 8 * u, to - 8 * u, o[i]);
+              c[2 * u] &= ~(bad.x * 0xffu), c[2 * u + 1] &= ~(bad.y * 0xffu);
+            }
           }
         }
       }
-    }
-    typename P::vec pw[2][P::N];
-    P::make(w[0], pw[0]);
-    P::make(w[1], pw[1]);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const typename P::vec v_lo = P::codes(vc[i].x, vc[i].y), v_hi = P::codes(vc[i].z, vc[i].w);
-#pragma unroll
-      for (int e = P::N - 1; e >= 0; --e) {
-        o[i] = mfma(v_lo, pw[0][e], o[i]);
-        o[i] = mfma(v_hi, pw[1][e], o[i]);
-      }
-      if (i & 1) __builtin_amdgcn_sched_barrier(0);
-    }
-    if (more) load_values(k0 + kStep, ps_next);
-    pk = pk_next, ps = ps_next, ks = ks_next, vs = vs_next;
-    pk_next = page_of(k0 + 2 * kStep + 16 * kg), ps_next = page_of(k0 + 2 * kStep + 16 * g);
-  }
-  l += __shfl_xor(l, 16, 64);
-  l += __shfl_xor(l, 32, 64);
-
-  // Join the waves by their maxima and sums; rows pass through LDS two waves' at a time, so that two workgroups'
-  // fit a CU with room to spare.
-  __syncthreads();  // the queries have been read
-  if (g == 0) s_m[wave][r] = m;
-  __syncthreads();
-  float mm = s_m[0][r];
-#pragma unroll
-  for (int k = 1; k < kWaves; ++k) mm = fmaxf(mm, s_m[k][r]);
-  const float a = mm == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - mm);
-  if (g == 0) s_l[wave][r] = a * l;
-#pragma unroll
-  for (int i = 0; i < MT; ++i) o[i] *= a;
-#pragma unroll
-  for (int turn = 0; turn < 2; ++turn) {
-    if (live && (turn ? wave < 2 : wave >= 2)) {
+      typename P::vec pw[2][P::N];
+      P::make(w[0], pw[0]);
+      P::make(w[1], pw[1]);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        f32x4* sum = reinterpret_cast<f32x4*>(&s_o[wave & 1][r][i * 16 + g * 4]);
-        *sum = turn ? *sum + o[i] : o[i];
+        const typename P::vec v_lo = P::codes(vc[i].x, vc[i].y), v_hi = P::codes(vc[i].z, vc[i].w);
+#pragma unroll
+        for (int e = P::N - 1; e >= 0; --e) {
+          o[i] = mfma(v_lo, pw[0][e], o[i]);
+          o[i] = mfma(v_hi, pw[1][e], o[i]);
+        }
+        if (i & 1) __builtin_amdgcn_sched_barrier(0);
+      }
+      if (more) load_values(k0 + kStep, ps_next);
+      pk = pk_next, ps = ps_next, ks = ks_next, vs = vs_next;
+      pk_next = page_of(k0 + 2 * kStep + 16 * kg), ps_next = page_of(k0 + 2 * kStep + 16 * g);
+    }
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+
+    // Join the waves by their maxima and sums; rows pass through LDS two waves' at a time, so that two workgroups'
+    // fit a CU with room to spare.
+    __syncthreads();  // the queries have been read
+    if (g == 0) s_m[wave][r] = m;
+    __syncthreads();
+    float mm = s_m[0][r];
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) mm = fmaxf(mm, s_m[k][r]);
+    const float a = lower(l, mm == -__builtin_inff() ? mm : m - mm);
+    if (g == 0) s_l[wave][r] = l;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[i] *= a;
+#pragma unroll
+    for (int turn = 0; turn < 2; ++turn) {
+      if (live && (turn ? wave < 2 : wave >= 2)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          f32x4* sum = reinterpret_cast<f32x4*>(&s_o[wave & 1][r][i * 16 + g * 4]);
+          *sum = turn ? *sum + o[i] : o[i];
+        }
+      }
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < kRows * D / 4; i += kWaves * 64) {
+      const int rr = i / (D / 4), c = (i - rr * (D / 4)) * 4, out_row = tile.first + rr;
+      if (out_row >= tile.rows) break;
+      float top = s_m[0][rr], ll = 0.f;
+#pragma unroll
+      for (int k = 1; k < kWaves; ++k) top = fmaxf(top, s_m[k][rr]);
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) ll += s_l[k][rr];
+      const f32x4 sum = *reinterpret_cast<const f32x4*>(&s_o[0][rr][c]) + *reinterpret_cast<const f32x4*>(&s_o[1][rr][c]);
+      const int64_t token = tile.begin + out_row / group;
+      const int h = head * group + out_row % group;
+      const int64_t out = token * p.h_q + h;
+      if (ns == 1) {
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        put<T>(p, sum * inv, token, (int64_t)h * D + c);
+        if (p.lse && c == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (top + __log2f(ll)) * 0.69314718055994530942f;
+      } else {
+        const int64_t part = SHARES ? piece * kRows + rr : piece * p.tokens * p.h_q + out;
+        *reinterpret_cast<f32x4*>(p.part_o + part * D + c) = sum;
+        if (c == 0) p.part_ml[2 * part] = top, p.part_ml[2 * part + 1] = ll;
       }
     }
-    __syncthreads();
-  }
-  for (int i = threadIdx.x; i < kRows * D / 4; i += kWaves * 64) {
-    const int rr = i / (D / 4), c = (i - rr * (D / 4)) * 4, out_row = tile.first + rr;
-    if (out_row >= tile.rows) break;
-    float top = s_m[0][rr], ll = 0.f;
-#pragma unroll
-    for (int k = 1; k < kWaves; ++k) top = fmaxf(top, s_m[k][rr]);
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) ll += s_l[k][rr];
-    const f32x4 sum = *reinterpret_cast<const f32x4*>(&s_o[0][rr][c]) + *reinterpret_cast<const f32x4*>(&s_o[1][rr][c]);
-    const int64_t token = tile.begin + out_row / group;
-    const int h = head * group + out_row % group;
-    const int64_t out = token * p.h_q + h;
-    if (ns == 1) {
-      const float inv = ll == 0.f ? 0.f : 1.f / ll;
-      put<T>(p, sum * inv, token, (int64_t)h * D + c);
-      if (p.lse && c == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (top + __log2f(ll)) * 0.69314718055994530942f;
-    } else {
-      const int64_t part = SHARES ? piece * kRows + rr : piece * p.tokens * p.h_q + out;
-      *reinterpret_cast<f32x4*>(p.part_o + part * D + c) = sum;
-      if (c == 0) p.part_ml[2 * part] = top, p.part_ml[2 * part + 1] = ll;
-    }
-  }
-  if constexpr (SHARES) __syncthreads();  // the next tile's queries take the sums' place
+    if constexpr (SHARES) __syncthreads();  // the next tile's queries take the sums' place
   }
 }
 
@@ -654,9 +673,8 @@ __global__ __launch_bounds__(kWaves * 64, sizeof(T) == 4 && D == 256 ? 1 : 2) vo
     const int row = tile.first + wave * 32 + c;
     const bool live = row < tile.rows;
     const int tok = row / group, hq = head * group + (row - tok * group);
-    const int pos = tile.ctx - tile.len + tok;
-    row_hi = live ? (p.causal ? min(tile.ctx, pos + 1) : tile.ctx) : 0;
-    row_lo = live && p.window ? pos - p.window + 1 : 0;
+    row_hi = live ? keys_to(p, tile, tok) : 0;
+    row_lo = live ? keys_from(p, tile, tok) : 0;
 #pragma unroll
     for (int k = 0; k < 2 * KB; ++k) {
       const int at = (k / 2) * 32 + h * 16 + (k & 1) * 8;
@@ -783,7 +801,6 @@ __global__ __launch_bounds__(kWaves * 64, sizeof(T) == 4 && D == 256 ? 1 : 2) vo
       // (a scale of zero: scores of zero, and no 0 * infinity where they are masked)
       const float unit = Pages::of(pages.ks, 2 * u + h) * p.scale_log2, f = held ? (unit == 0.f ? 1e-30f : unit) : 1.f;
       const float vs = held ? Pages::of(pages.vs, 2 * u + h) : 1.f;
-      const float lv = fminf(fmaxf(__log2f(fabsf(vs)), -40.f), 120.f);
 
       f32x16 s = zeros16();
       const int keys = half * kBytes + 32 * u * D + key_at;
@@ -814,17 +831,16 @@ __global__ __launch_bounds__(kWaves * 64, sizeof(T) == 4 && D == 256 ? 1 : 2) vo
       float top = fmaxf(s[0], s[1]);
 #pragma unroll
       for (int e = 2; e < 16; e += 2) top = max3(top, s[e], s[e + 1]);
-      top = half_max(fmaf(top, f, lv));
+      top = half_max(fmaf(top, f, log2_scale(vs)));
       // the maximum moves only where it grows by more than 2^8: the weights then stay under 256
       if (__any(top > m + 8.f)) {
         const float now = fmaxf(m, top);
-        const float alpha = now == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - now);
+        const float alpha = lower(l, now == -__builtin_inff() ? now : m - now);
         m = now;
-        l *= alpha;
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[i] *= alpha;
       }
-      const float base = m == -__builtin_inff() ? 0.f : m;
+      const float base = (m == -__builtin_inff() ? 0.f : m) - kUp, factor = vs * kDown;
       typename P::vec pw[2][P::N];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -832,8 +848,8 @@ __global__ __launch_bounds__(kWaves * 64, sizeof(T) == 4 && D == 256 ? 1 : 2) vo
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           w[e] = __builtin_amdgcn_exp2f(fmaf(s[8 * j + e], f, -base));
-          l += w[e];
-          w[e] *= vs;
+          l = fmaf(w[e], kDown, l);
+          w[e] *= factor;
         }
         P::make(w, pw[j]);
       }
@@ -953,8 +969,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttendParams p) {
     float a = 0.f;
     if (s0 + lane < ns) {
       const int64_t part = (s0 + lane) * step + part0;
-      a = __builtin_amdgcn_exp2f(p.part_ml[2 * part] - base);
-      ll += a * p.part_ml[2 * part + 1];
+      float l = p.part_ml[2 * part + 1];
+      a = lower(l, p.part_ml[2 * part] - base);
+      ll += l;
     }
     const int n = min(64, ns - s0);
     for (int s = 0; s < n; ++s) {
@@ -1018,7 +1035,8 @@ Plan plan(const AttendShape& a) {
   // the longest contexts would give each at least 4 steps.
   const int64_t at_once = 256 * (a.d != 64 ? 2 : a.bf16 ? 4 : 3);
   c.shares = 0;
-  if (!c.chunk && !a.ragged && c.slots <= kMostTiles && tiles * ((most + kStep - 1) / kStep) >= 4 * at_once) c.shares = (int32_t)at_once;
+  const int64_t steps = c.slots * ((most + kStep - 1) / kStep);  // of one head, added up in 32 bits
+  if (!c.chunk && !a.ragged && c.slots <= kMostTiles && steps <= INT32_MAX && steps * a.h_kv >= 4 * at_once) c.shares = (int32_t)at_once;
   c.parts = c.shares ? (c.shares + tiles) * kRows : c.pieces > 1 ? c.pieces * a.tokens * a.h_q : 0;
   return c;
 }

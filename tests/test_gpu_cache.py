@@ -462,3 +462,36 @@ def test_offsets_beyond_32_bits():
                 tokens = min(max(int(lens[n]) - j * page, 0), page)
                 assert torch.equal(big.k[a].view(torch.uint8)[:, :tokens], small.k[b].view(torch.uint8)[:, :tokens])
                 assert torch.equal(big.v[a].view(torch.uint8)[..., :tokens], small.v[b].view(torch.uint8)[..., :tokens])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new,width", [([1, 1], None), ([1, 1], 2048), ([70, 40], None)])  # pieces, shares, a chunk
+@pytest.mark.parametrize("sizes", [(1e37,), (1e-22,), (1.0, 1e37), (1e37, 1.0, 1e30, 0.0), (0.0,), (0.0, 1.0)])
+def test_sizes_of_values(sizes, new, width, dtype):
+    """Values from the type's largest to its small ones, pages of zeros among them: e^(score - max) of what counts
+    passes neither end of fp32, whatever the maximum of score + log scale is."""
+    gen = torch.Generator().manual_seed(90)
+    page, d, heads, ctx = 64, 64, 2, [777, 300]
+    table, pages = tables(gen, ctx, page, width=width)
+    cache = pool(pages, heads, d, page)
+    T = sum(ctx)
+    k, v = rand(gen, T, heads, d, dtype), torch.randn((T, heads, d), generator=gen)
+    size = torch.tensor(sizes).repeat(-(-T // page // len(sizes)) + 1).repeat_interleave(page)[:T]
+    v = (v.clamp(-3, 3) * size[:, None, None]).to(dtype).cuda()
+    gdn.cache_store(k, v, cache, table, ints([0, 0]), cu_of(ctx))
+    q = (2.0 * torch.randn((sum(new), 4, d), generator=gen)).to(dtype).cuda()
+    cu = None if new[0] == 1 else cu_of(new)
+    got = gdn.cache_attention(q, cache, table, ints(ctx), cu, return_lse=True)
+    ref.close_attention(got, ref.cache_attention(q, cache, table, ints(ctx), cu), str(sizes))
+
+
+@pytest.mark.parametrize("new", [[1, 1], [3, 2], [100, 60]])
+def test_windows_of_any_size(new):
+    """A window as wide as 32 bits allow is none at all, also for rows whose position lies before the first token."""
+    gen = torch.Generator().manual_seed(91)
+    cache, table = filled(gen, [1500, 50], 2, 64, 64)
+    q = torch.randn((sum(new), 8, 64), generator=gen).to(BF16).cuda()
+    for causal in (True, False):
+        want = gdn.cache_attention(q, cache, table, ints([1500, 50]), cu_of(new), causal=causal)
+        for window in (1501, 2 ** 30, 2 ** 31 - 1):
+            assert torch.equal(gdn.cache_attention(q, cache, table, ints([1500, 50]), cu_of(new), causal=causal, window=window), want)
