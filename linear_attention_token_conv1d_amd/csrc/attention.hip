@@ -40,6 +40,7 @@
 #include "sequences.h"
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 namespace gdn {
@@ -1025,17 +1026,25 @@ Plan plan(const AttendShape& a) {
   Plan c;
   const int64_t group = a.h_q / a.h_kv;
   c.uniform = a.tokens / a.n_seqs;
-  // Sequences of 64 rows and more on average share their keys among a workgroup's waves.
-  c.chunk = a.tokens * group >= (int64_t)a.n_seqs * 64;
+  // Rows of 128 share their keys among a workgroup's waves where a sequence has at least two tiles of 16 (averages;
+  // 32 sequences of 4096 tokens, 4 heads of 256: 73 against 85 us with 12 rows, 110 against 89 with 24), and all of
+  // them enough for that kernel's fewer and longer workgroups (one sequence of 8192: 38 against 36 us with 24 tiles in
+  // all, 24 against 35 with 8).  In fp32 the chunk kernel holds the queries as three times as many registers, half the
+  // waves: from three tiles with heads of 256 (150 against 205 us, 257 against 216 with 36 rows), from 400 rows with
+  // smaller ones (one sequence of 8192, heads of 128: 42 against 44 us with 288 rows, 110 against 100 with 1200).
+  const double rows = (double)a.tokens * group / a.n_seqs, all = a.n_seqs * std::ceil(rows / kRows) * a.h_kv;
+  const int least = a.bf16 ? kRows : a.d == 256 ? 2 * kRows : 400;
+  c.chunk = rows > least && all >= (a.d == 256 ? 24 : 32);
   c.tile_rows = !c.chunk ? kRows : kChunkRows;
   c.uniform_tiles = (int32_t)((c.uniform * group + c.tile_rows - 1) / c.tile_rows);
   c.slots = a.ragged ? a.tokens * group / c.tile_rows + a.n_seqs : (int64_t)c.uniform_tiles * a.n_seqs;
-  // Pieces of the contexts, for enough workgroups.  Single tokens: about 4096 (16 for each CU), of at least 256
-  // tokens, a turn of a workgroup's four waves.  Chunks: about 1024 where there are fewer than 512 without pieces,
-  // of at least 512 tokens.
-  const int64_t most = max_tokens(a), step = c.chunk ? 512 : kStep, tiles = c.slots * a.h_kv;
+  // Pieces of the contexts, for enough workgroups: of single tokens about 4096 (16 for each CU), of chunks 512, as many
+  // as run at once, where there are fewer without pieces (one sequence of 8192, 4 heads of 256: 1200 rows take 81 us, 94
+  // in 1024 pieces).  Both of at least 256 tokens, a turn of the waves of a workgroup with single tokens (102 rows: 32 us,
+  // 39 with 512).
+  const int64_t most = max_tokens(a), step = kStep, tiles = c.slots * a.h_kv;
   int64_t piece = most;
-  if (!c.chunk || tiles < 512) piece = (int64_t)std::min((double)most, (double)most * tiles / (c.chunk ? 1024 : 4096));
+  if (!c.chunk || tiles < 512) piece = (int64_t)std::min((double)most, (double)most * tiles / (c.chunk ? 512 : 4096));
   piece = (piece + step - 1) / step * step;
   c.piece = (int32_t)(piece < step ? step : piece);
   c.pieces = (most + c.piece - 1) / c.piece;
