@@ -239,8 +239,9 @@ __device__ __forceinline__ float lower(float& l, float x) {
   return half * half;
 }
 
-// 16 bytes that no other workgroup reads soon: nontemporal (a decode step of 64 sequences of up to 32768 tokens 386 ->
-// 364 us; fp32 queries, whose registers do not suffice, are the better without: 618 against 631).
+// 16 bytes that nobody reads soon again: nontemporal (a decode step of 64 sequences of up to 32768 tokens 386 -> 364 us;
+// fp32 queries, whose registers do not suffice, are the better without: 618 against 631).  Not so values of pages
+// beyond 64 tokens, where two waves take the halves of a cache line (pages of 128, up to 16384 tokens: 297 -> 271 us).
 template <bool STREAM>
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
   if constexpr (!STREAM) return *reinterpret_cast<const uint4*>(p);
@@ -301,7 +302,8 @@ __device__ __forceinline__ void place_tiles(const AttendParams& p, int group, in
   __syncthreads();
 }
 
-template <typename T, int D, bool SHARES>
+// WIDE: pages of more than 64 tokens.
+template <typename T, int D, bool SHARES, bool WIDE>
 __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int NQ = F32 ? 3 : 1;
@@ -378,7 +380,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attend_kernel(AttendParams p) 
     auto load_values = [&](int k0, int ps) {
       const uint8_t* vp = p.v_cache + ((((int64_t)inside(ps) * p.h_kv + head) * D + r) << p.page_shift) + ((k0 + 16 * g) & in_page);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) vc[i] = load_codes<!F32>(vp + ((i * 16) << p.page_shift));
+      for (int i = 0; i < MT; ++i) vc[i] = load_codes<!F32 && !WIDE>(vp + ((i * 16) << p.page_shift));
     };
     const int k_first = start + wave * kTok;
     int pk = page_of(k_first + 16 * kg), ps = page_of(k_first + 16 * g);
@@ -1063,8 +1065,11 @@ template <typename T, int D>
 hipError_t launch(const AttendParams& p, const Plan& c, hipStream_t stream) {
   const int64_t rows = p.cu_seqlens ? c.tile_rows : std::min((int64_t)c.tile_rows, c.uniform * (p.h_q / p.h_kv));
   const dim3 block(kWaves * 64), joins((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)rows);
+  constexpr bool kWide = sizeof(T) == 2;  // fp32 has one form
+  const bool wide = kWide && p.page_shift > 6;
   if (c.shares) {
-    hipLaunchKernelGGL((attend_kernel<T, D, true>), dim3((unsigned)c.shares), block, 0, stream, p);
+    if (wide) hipLaunchKernelGGL((attend_kernel<T, D, true, kWide>), dim3((unsigned)c.shares), block, 0, stream, p);
+    else hipLaunchKernelGGL((attend_kernel<T, D, true, false>), dim3((unsigned)c.shares), block, 0, stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((join_kernel<T, D, true>), joins, block, 0, stream, p);
@@ -1073,7 +1078,8 @@ hipError_t launch(const AttendParams& p, const Plan& c, hipStream_t stream) {
   const int64_t turns = (c.slots * p.h_kv + 7) / 8;
   if (turns > INT32_MAX / 8) return hipErrorInvalidValue;
   const dim3 grid((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)c.pieces), chunks((unsigned)(turns * 8), (unsigned)c.pieces);
-  if (!c.chunk) hipLaunchKernelGGL((attend_kernel<T, D, false>), grid, block, 0, stream, p);
+  if (!c.chunk && wide) hipLaunchKernelGGL((attend_kernel<T, D, false, kWide>), grid, block, 0, stream, p);
+  else if (!c.chunk) hipLaunchKernelGGL((attend_kernel<T, D, false, false>), grid, block, 0, stream, p);
   else if (p.page_shift >= 6) hipLaunchKernelGGL((attend_chunk_kernel<T, D, true>), chunks, block, 0, stream, p);
   else hipLaunchKernelGGL((attend_chunk_kernel<T, D, false>), chunks, block, 0, stream, p);
   const hipError_t e = hipGetLastError();
