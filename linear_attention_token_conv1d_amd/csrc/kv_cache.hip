@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreParams p) {
   const int64_t begin = p.cu_seqlens ? max(as_const(p.cu_seqlens)[n], 0) : (int64_t)n * p.uniform;
   const int64_t end = p.cu_seqlens ? min((int64_t)as_const(p.cu_seqlens)[n + 1], p.tokens) : begin + p.uniform;
   const int64_t held = as_const(p.lens)[n];  // tokens of the sequence in the cache
-  if (held < 0 || end <= begin) return;
+  if (held < 0 || end <= begin || j < 0) return;  // (slots ahead of a pack that does not begin at token 0)
   const int64_t first = (held / p.page + j) * p.page;  // the page's first position
   if (first >= held + (end - begin) || first / p.page >= p.max_pages) return;
   // slots [a, b) of the page get the tokens from row on

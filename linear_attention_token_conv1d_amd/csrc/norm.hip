@@ -93,7 +93,7 @@ __device__ __forceinline__ void group_sum(float (&a)[N]) {
 template <typename T, int VEC, int G, int NV>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
   const int lane = threadIdx.x % G;
-  int64_t row = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G;
+  int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kThreads / G) + threadIdx.x / G;
   const bool live = row < p.rows;
   if (!live) row = p.rows - 1;  // a surplus group follows along without storing
   const uint32_t t = (uint32_t)row / (uint32_t)p.heads;
@@ -361,9 +361,10 @@ struct Forward {
   hipStream_t stream;
   template <int VEC, int G, int NV>
   hipError_t operator()() const {
-    const int64_t per = kThreads / G;
-    hipLaunchKernelGGL((norm_kernel<T, VEC, G, NV>), dim3((unsigned)((p.rows + per - 1) / per)), dim3(kThreads), 0,
-                       stream, p);
+    // a grid's first side holds less than 2^32 threads: 2^22 workgroups, and as many sides as it takes
+    const int64_t per = kThreads / G, need = (p.rows + per - 1) / per, side = need < (1 << 22) ? need : 1 << 22;
+    hipLaunchKernelGGL((norm_kernel<T, VEC, G, NV>), dim3((unsigned)side, (unsigned)((need + side - 1) / side)), dim3(kThreads),
+                       0, stream, p);
     return hipGetLastError();
   }
 };

@@ -495,3 +495,26 @@ def test_windows_of_any_size(new):
         want = gdn.cache_attention(q, cache, table, ints([1500, 50]), cu_of(new), causal=causal)
         for window in (1501, 2 ** 30, 2 ** 31 - 1):
             assert torch.equal(gdn.cache_attention(q, cache, table, ints([1500, 50]), cu_of(new), causal=causal, window=window), want)
+
+
+@pytest.mark.parametrize("new", [[5, 20, 0, 1], [150, 40, 0, 200]])
+def test_pack_that_begins_behind_the_first_token(new):
+    """Offsets that start above 0: the tokens ahead of the first sequence and behind the last are left alone."""
+    gen = torch.Generator().manual_seed(92)
+    page, d, skip, behind = 16, 64, 100, 30
+    old = [3, 50, 7, 31]
+    total = [a + b for a, b in zip(old, new)]
+    cu = cu_of(new) + skip
+    cu = cu.to(torch.int32)
+    table, pages = tables(gen, total, page)
+    cache = pool(pages, 2, d, page)
+    k = rand(gen, sum(old), 2, d, BF16)
+    check_store(k, -k, cache, table, ints([0] * 4), cu_of(old), "old")
+    T = skip + sum(new) + behind
+    k = rand(gen, T, 2, d, BF16, scale=3.0)
+    check_store(k, -k, cache, table, ints(old), cu, "new")
+    q = torch.randn((T, 8, d), generator=gen).to(BF16).cuda()
+    out = torch.full_like(q, 7.0)
+    got = gdn.cache_attention(q, cache, table, ints(total), cu, out=out, return_lse=True)
+    assert torch.all(out[:skip] == 7.0) and torch.all(out[skip + sum(new):] == 7.0)
+    ref.close_attention(got, ref.cache_attention(q, cache, table, ints(total), cu), "offset")

@@ -227,3 +227,13 @@ def test_small_rows_without_eps():
     dx = gdn.rms_norm_backward(x, dy, eps=0.0)[0]
     rh, sh, *_ = ref.rms_norm_backward(x, dy, None, None, None, "pre", "silu", 1.0, 0.0, 0.0)
     ref.close(dx, rh, sh, 64, "dx")
+
+
+def test_more_rows_than_one_side_of_a_grid():
+    """Rows of a workgroup each whose threads pass 32 bits."""
+    T, D = (1 << 24) + 77, 1032
+    x = torch.empty((T, D), dtype=BF16, device="cuda")
+    tail = torch.randn((100, D), generator=torch.Generator().manual_seed(11)).to(BF16).cuda()
+    x[-100:] = tail
+    gdn.rms_norm(x, out=x)
+    assert torch.equal(x[-100:], gdn.rms_norm(tail))
