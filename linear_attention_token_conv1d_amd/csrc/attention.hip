@@ -934,9 +934,10 @@ __global__ __launch_bounds__(kWaves * 64, sizeof(T) == 4 && D == 256 ? 1 : 2) vo
   }
 }
 
-// Joins the pieces of a row: a workgroup a row, its lanes over the head's elements, its waves over the pieces, each
-// eight at a time on their way (a wave a row and one piece after another: 33 of the 45 us that a context of 32768
-// tokens in 128 pieces took).
+// Joins the pieces of a row, its lanes over the head's elements, eight pieces at a time on their way.  Where there may
+// be more than eight a workgroup's four waves share a row (one token over 32768 in 128 pieces: 24 us in all, 45 with one
+// piece after another), otherwise each has its own (538 tokens of 32 heads of 256 in up to 4
+// pieces: 18 us, 47 with a workgroup a row).
 constexpr int kJoin = 8;
 template <typename T, int D, bool SHARES>
 __global__ __launch_bounds__(kWaves * 64) void join_kernel(AttendParams p) {
@@ -945,7 +946,7 @@ __global__ __launch_bounds__(kWaves * 64) void join_kernel(AttendParams p) {
   const int group = p.h_q / p.h_kv, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Tile tile = find_tile(p, blockIdx.x, group, p.tile_rows);
   if (!tile.some) return;
-  const int at = tile.first + blockIdx.z;
+  const int share = p.join_waves == 1 ? 0 : wave, at = tile.first + (p.join_waves == 1 ? (int)blockIdx.z * kWaves + wave : (int)blockIdx.z);
   int ns;
   int64_t part0 = 0;  // the first partial result's row
   if constexpr (SHARES) {
@@ -971,11 +972,11 @@ __global__ __launch_bounds__(kWaves * 64) void join_kernel(AttendParams p) {
   float sum[E], ll = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = 0.f;
-  for (int s0 = wave; s0 < ns; s0 += kWaves * kJoin) {
+  for (int s0 = share; s0 < ns; s0 += p.join_waves * kJoin) {
     float row[kJoin][E], ml[kJoin][2];
 #pragma unroll
     for (int j = 0; j < kJoin; ++j) {
-      const int64_t part = min(s0 + j * kWaves, ns - 1) * step + part0;
+      const int64_t part = min(s0 + j * p.join_waves, ns - 1) * step + part0;
       ml[j][0] = p.part_ml[2 * part], ml[j][1] = p.part_ml[2 * part + 1];
 #pragma unroll
       for (int e = 0; e < E; ++e) row[j][e] = p.part_o[part * D + lane * E + e];
@@ -983,12 +984,24 @@ __global__ __launch_bounds__(kWaves * 64) void join_kernel(AttendParams p) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < kJoin; ++j) {
-      const bool there = s0 + j * kWaves < ns;  // (those behind the last are the last again)
+      const bool there = s0 + j * p.join_waves < ns;  // (those behind the last are the last again)
       const float f = lower(ml[j][1], ml[j][0] - base), a = there ? f : 0.f;
       ll += there ? ml[j][1] : 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) sum[e] = fmaf(a, row[j][e], sum[e]);
     }
+  }
+  if (p.join_waves == 1) {
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int64_t c = (int64_t)h * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float y = sum[e] * inv;
+      if (p.gate) y = gated<T>(y, to_f32(reinterpret_cast<const T*>(p.gate)[token * p.gate_stride + c + e]));
+      reinterpret_cast<T*>(p.o)[token * p.o_stride + c + e] = from_f32<T>(y);
+    }
+    if (p.lse && lane == 0) p.lse[out] = ll == 0.f ? -__builtin_inff() : (mm + __log2f(ll)) * 0.69314718055994530942f;
+    return;
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) s_sum[wave][lane * E + e] = sum[e];
@@ -1015,6 +1028,7 @@ struct Plan {
   int32_t piece;
   int64_t pieces;  // of the longest context that the table holds
   int32_t shares;  // 0: pieces
+  int32_t join_waves;  // that join a row
   int64_t parts;   // rows of partial results
 };
 
@@ -1040,13 +1054,16 @@ Plan plan(const AttendShape& a) {
   c.tile_rows = !c.chunk ? kRows : kChunkRows;
   c.uniform_tiles = (int32_t)((c.uniform * group + c.tile_rows - 1) / c.tile_rows);
   c.slots = a.ragged ? a.tokens * group / c.tile_rows + a.n_seqs : (int64_t)c.uniform_tiles * a.n_seqs;
-  // Pieces of the contexts, for enough workgroups: of single tokens about 4096 (16 for each CU), of chunks 512, as many
-  // as run at once, where there are fewer without pieces (one sequence of 8192, 4 heads of 256: 1200 rows take 81 us, 94
-  // in 1024 pieces).  Both of at least 256 tokens, a turn of the waves of a workgroup with single tokens (102 rows: 32 us,
+  // Pieces of the contexts, for enough workgroups: of single tokens about 4096 (16 for each CU), of chunks at most 512, as
+  // many as run at once (one sequence of 8192, 4 heads of 256: 1200 rows take 81 us, 94 in 1024 pieces; two of 4000 with
+  // 7800 rows, 488 tiles, 251 us whole, 382 in twice as many).  Both of at least 256 tokens, a turn of the waves of a workgroup with single tokens (102 rows: 32 us,
   // 39 with 512).
-  const int64_t most = max_tokens(a), step = kStep, tiles = c.slots * a.h_kv;
-  int64_t piece = most;
-  if (!c.chunk || tiles < 512) piece = (int64_t)std::min((double)most, (double)most * tiles / (c.chunk ? 512 : 4096));
+  // (a causal window bounds the keys of a tile: those of its first token's window to its last token)
+  int64_t most = max_tokens(a);
+  if (a.causal && a.window > 0) most = std::min(most, (int64_t)a.window + (c.tile_rows - 1) / group + kTok);
+  const int64_t step = kStep, tiles = c.slots * a.h_kv;
+  int64_t piece = (int64_t)std::min((double)most, (double)most * tiles / 4096);
+  if (c.chunk) piece = tiles < 512 ? (most + 512 / tiles - 1) / (512 / tiles) : most;
   piece = (piece + step - 1) / step * step;
   c.piece = (int32_t)(piece < step ? step : piece);
   c.pieces = (most + c.piece - 1) / c.piece;
@@ -1057,6 +1074,7 @@ Plan plan(const AttendShape& a) {
   c.shares = 0;
   const int64_t steps = c.slots * ((most + kStep - 1) / kStep);  // of one head, added up in 32 bits
   if (!c.chunk && !a.ragged && c.slots <= kMostTiles && steps <= INT32_MAX && steps * a.h_kv >= 4 * at_once) c.shares = (int32_t)at_once;
+  c.join_waves = (c.shares ? c.shares / tiles : c.pieces) > 8 ? kWaves : 1;
   c.parts = c.shares ? (c.shares + tiles) * kRows : c.pieces > 1 ? c.pieces * a.tokens * a.h_q : 0;
   return c;
 }
@@ -1064,7 +1082,7 @@ Plan plan(const AttendShape& a) {
 template <typename T, int D>
 hipError_t launch(const AttendParams& p, const Plan& c, hipStream_t stream) {
   const int64_t rows = p.cu_seqlens ? c.tile_rows : std::min((int64_t)c.tile_rows, c.uniform * (p.h_q / p.h_kv));
-  const dim3 block(kWaves * 64), joins((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)rows);
+  const dim3 block(kWaves * 64), joins((unsigned)c.slots, (unsigned)p.h_kv, (unsigned)(p.join_waves == 1 ? (rows + kWaves - 1) / kWaves : rows));
   constexpr bool kWide = sizeof(T) == 2;  // fp32 has one form
   const bool wide = kWide && p.page_shift > 6;
   if (c.shares) {
@@ -1118,6 +1136,7 @@ hipError_t launch_attend(AttendParams p, const AttendShape& a, void* workspace, 
   p.tile_rows = c.tile_rows;
   p.slots = (int32_t)c.slots;
   p.shares = c.shares;
+  p.join_waves = c.join_waves;
   if (c.parts) {
     char* w = reinterpret_cast<char*>(workspace);
     p.part_o = reinterpret_cast<float*>(w);

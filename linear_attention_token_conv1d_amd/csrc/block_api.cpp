@@ -102,7 +102,7 @@ bool attend_shape(const gdn_cache_attention_args* a, gdn::AttendShape* s) {
       a->tokens > INT32_MAX / (a->h_q / a->h_kv) / 2)
     return false;
   *s = gdn::AttendShape{a->tokens, a->n_seqs, a->h_q, a->h_kv, a->d, a->page_size, a->max_pages, a->cu_seqlens ? 1 : 0,
-                        a->io_dtype == GDN_BF16 ? 1 : 0};
+                        a->io_dtype == GDN_BF16 ? 1 : 0, a->causal, a->window};
   return true;
 }
 
@@ -358,7 +358,7 @@ gdn_status gdn_cache_attention(const gdn_cache_attention_args* a, void* stream) 
     gdn::AttendParams p{a->q, static_cast<const uint8_t*>(a->k_cache), static_cast<const uint8_t*>(a->v_cache), a->k_scale,
                         a->v_scale, a->page_table, a->lens, a->cu_seqlens, a->gate, a->o, a->lse, a->q_stride, a->gate_stride,
                         a->o_stride, a->tokens, a->n_seqs, a->h_q, a->h_kv, shift, a->pages, a->max_pages, a->causal,
-                        a->window, a->scale * 1.44269504088896340736f, 0, 0, 0, 0, 0, 0, 0, nullptr, nullptr, nullptr};
+                        a->window, a->scale * 1.44269504088896340736f, 0, 0, 0, 0, 0, 0, 0, 0, nullptr, nullptr, nullptr};
     hipStream_t s = static_cast<hipStream_t>(stream);
     return finish(gdn::launch_attend(p, shape, a->workspace, a->io_dtype, s), s, f);
   } catch (...) {

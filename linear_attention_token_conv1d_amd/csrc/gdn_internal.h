@@ -262,6 +262,8 @@ struct AttendShape {
   int32_t max_pages;
   int32_t ragged;
   int32_t bf16;
+  int32_t causal;
+  int32_t window;  // 0 (or less): none
 };
 struct AttendParams {
   const void* q;
@@ -296,6 +298,7 @@ struct AttendParams {
   int32_t tile_rows;
   int32_t slots;
   int32_t shares;
+  int32_t join_waves;
   float* part_o;    // [pieces, tokens, h_q, d], or [shares + tiles, 16, d]
   float* part_ml;   // a maximum and a sum for each of those rows
   int32_t* places;  // [slots + 1] with shares

@@ -518,3 +518,18 @@ def test_pack_that_begins_behind_the_first_token(new):
     got = gdn.cache_attention(q, cache, table, ints(total), cu, out=out, return_lse=True)
     assert torch.all(out[:skip] == 7.0) and torch.all(out[skip + sum(new):] == 7.0)
     ref.close_attention(got, ref.cache_attention(q, cache, table, ints(total), cu), "offset")
+
+
+@pytest.mark.parametrize("window", [1, 63, 64, 65, 300, 1000])
+@pytest.mark.parametrize("new,h_q", [([1] * 3, 4), ([5, 0, 9], 2), ([1] * 3, 40), ([60, 33, 1], 6), ([300, 1, 131], 2)])
+def test_windows_in_long_tables(new, h_q, window):
+    """Windows well inside long contexts and longer tables: pieces are cut for the window's keys."""
+    gen = torch.Generator().manual_seed(93)
+    ctx = [2000, 1, 1537]
+    cache, table = filled(gen, ctx, 2, 64, 32, width=400)
+    q = torch.randn((sum(new), h_q, 64), generator=gen).to(BF16).cuda()
+    cu = None if len(set(new)) == 1 else cu_of(new)
+    need = gdn.cache_attention_workspace_size(sum(new), 3, 400, h_q, 2, 64, 32, cu is not None, window=window)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda") if need else None
+    got = gdn.cache_attention(q, cache, table, ints(ctx), cu, window=window, return_lse=True, workspace=ws)
+    ref.close_attention(got, ref.cache_attention(q, cache, table, ints(ctx), cu, window=window), f"window {window}")
