@@ -229,7 +229,7 @@ def cache_attention(q, cache, page_table, lens, cu_seqlens=None, scale=None, cau
 
 def cache_attention_workspace_size(tokens, n_seqs, max_pages, h_q, h_kv, d, page_size=64, ragged=False, dtype=torch.bfloat16,
                                    causal=True, window=0):
-    """Bytes of workspace that cache_attention needs (0: none) for a caller that keeps one."""
+    """Bytes of workspace that cache_attention needs with these arguments (0: none), for a caller that keeps one."""
     a = CacheAttentionArgs(struct_size=ctypes.sizeof(CacheAttentionArgs), io_dtype=_DT[dtype], n_seqs=n_seqs, h_q=h_q, h_kv=h_kv, d=d, page_size=page_size,
                            max_pages=max_pages, tokens=tokens, cu_seqlens=1 if ragged else None, causal=int(bool(causal)), window=window)
     return lib().gdn_cache_attention_workspace_size(a)
