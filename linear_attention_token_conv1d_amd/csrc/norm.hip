@@ -147,10 +147,13 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
   }
 }
 
-template <typename T, int VEC, int G, int NV>
-__global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p, float* partial) {
+// GATE: without one a wide row leaves registers for another workgroup (16384 rows of 5120: 275 -> 186 us; of 8192:
+// 387 -> 216).
+template <typename T, int VEC, int G, int NV, bool GATE>
+__global__ __launch_bounds__(kThreads, NV * VEC > 16 && NV * VEC <= 32 ? 2 : 1) void norm_backward_kernel(NormBwdParams p, float* partial) {
   constexpr int kGroups = kThreads / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  const bool gate = GATE && (NV > 2 || p.gate);  // (the test costs nothing and leaves short rows their registers: 124, 136 without)
   float dw[NV][VEC];
   Weight<VEC> w[NV];
 #pragma unroll
@@ -180,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p
       if (at >= p.width) continue;
       d.x[v] = load_pack<T, VEC>(p.x, t * p.x_stride + col + at);
       d.g[v] = load_pack<T, VEC>(p.dy, t * p.dy_stride + col + at);
-      if (p.gate) d.z[v] = load_pack<T, VEC>(p.gate, t * p.gate_stride + col + at);
+      if (gate) d.z[v] = load_pack<T, VEC>(p.gate, t * p.gate_stride + col + at);
       if (p.d_sum) d.ds[v] = load_pack<T, VEC>(p.d_sum, t * p.d_sum_stride + col + at);
     }
   };
@@ -195,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p
       for (int e = 0; e < VEC; ++e) {
         const float h = to_f32(d.x[v].v[e]);
         float u = to_f32(d.g[v].v[e]) * w[v].get(p.weight, p.weight_offset, e);
-        if (p.gate) {
+        if (gate) {
           const float z = to_f32(d.z[v].v[e]);
           s[v][e] = sigmoid<T>(z);
           u *= p.act == 1 ? z * s[v][e] : s[v][e];
@@ -221,7 +224,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p
         const float n = to_f32(d.x[v].v[e]) * r, dy = post * to_f32(d.g[v].v[e]), wt = w[v].get(p.weight, p.weight_offset, e);
         float a = 1.f;
         const float nd = dy * n;
-        if (p.gate) {
+        if (gate) {
           const float z = to_f32(d.z[v].v[e]), sg = s[v][e];
           a = p.act == 1 ? z * sg : sg;
           dz[e] = nd * wt * (p.act == 1 ? sg * (1.f + z * (1.f - sg)) : sg * (1.f - sg));
@@ -237,7 +240,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormBwdParams p
           for (int e = 0; e < VEC; ++e) dx[e] *= p.scale;
         store_pack<T, VEC>(p.dx, t * p.dx_stride + col + at, dx);
       }
-      if (p.gate) store_pack<T, VEC>(p.dgate, t * p.dgate_stride + col + at, dz);
+      if (gate) store_pack<T, VEC>(p.dgate, t * p.dgate_stride + col + at, dz);
     }
   };
 
@@ -322,6 +325,9 @@ bool vec_ok(const void* p, int64_t stride, int vec, size_t es) {
 
 // Calls f with the template arguments that fit a row: VEC elements a load,
 // groups of G lanes, NV loads a lane.  `vec`: whether 16-byte loads are aligned.
+// Heads of 128 with a wave each instead of 16 lanes: 231 us backward, 82 with;
+// rows of 512 with a workgroup instead of a wave: 198 and 110, of 1024: 128 and
+// 120.
 template <typename T, typename F>
 hipError_t dispatch(int width, bool vec, F&& f) {
   constexpr int V = 16 / (int)sizeof(T);
@@ -352,7 +358,8 @@ hipError_t dispatch(int width, bool vec, F&& f) {
 }
 
 // The most workgroups of the backward: enough to fill the chip, few enough
-// that their partial dw rows stay small beside the rows themselves.
+// that their partial dw rows stay small beside the rows themselves (8192 tokens
+// of 32 gated heads of 128: 82 us, 90 with 512, 86 with 2048).
 constexpr int kMostBlocks = 1024;
 int backward_blocks(int64_t rows) {
   return (int)(rows < kMostBlocks ? (rows > 0 ? rows : 1) : kMostBlocks);
@@ -379,9 +386,13 @@ struct Backward {
   template <int VEC, int G, int NV>
   hipError_t operator()() const {
     const int64_t need = (p.rows + kThreads / G - 1) / (kThreads / G);
+    // as many as run at once, or a whole number of times that: three of these run on a CU (65536 rows of 1024 without
+    // a gate: 131 us with 1024, 103 with 768), two or four of the others
+    if (sizeof(T) == 2 && G > 16 && NV <= 2 && VEC > 1 && !p.gate && *blocks > 768) *blocks = 768;
     if (need < *blocks) *blocks = (int)need;
-    hipLaunchKernelGGL((norm_backward_kernel<T, VEC, G, NV>), dim3((unsigned)*blocks), dim3(kThreads), 0, stream, p,
-                       p.dweight ? reinterpret_cast<float*>(p.workspace) : nullptr);
+    float* partial = p.dweight ? reinterpret_cast<float*>(p.workspace) : nullptr;
+    if (p.gate) hipLaunchKernelGGL((norm_backward_kernel<T, VEC, G, NV, true>), dim3((unsigned)*blocks), dim3(kThreads), 0, stream, p, partial);
+    else hipLaunchKernelGGL((norm_backward_kernel<T, VEC, G, NV, false>), dim3((unsigned)*blocks), dim3(kThreads), 0, stream, p, partial);
     return hipGetLastError();
   }
 };
