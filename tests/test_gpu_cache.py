@@ -465,7 +465,7 @@ def test_offsets_beyond_32_bits():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("new,width", [([1, 1], None), ([1, 1], 2048), ([70, 40], None)])  # pieces, shares, a chunk
+@pytest.mark.parametrize("new,width", [([1, 1], None), ([1, 1], 40), ([1, 1], 2048), ([70, 40], None)])  # whole, pieces, shares, a chunk
 @pytest.mark.parametrize("sizes", [(1e37,), (1e-22,), (1.0, 1e37), (1e37, 1.0, 1e30, 0.0), (0.0,), (0.0, 1.0)])
 def test_sizes_of_values(sizes, new, width, dtype):
     """Values from the type's largest to its small ones, pages of zeros among them: e^(score - max) of what counts
@@ -533,3 +533,34 @@ def test_windows_in_long_tables(new, h_q, window):
     ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda") if need else None
     got = gdn.cache_attention(q, cache, table, ints(ctx), cu, window=window, return_lse=True, workspace=ws)
     ref.close_attention(got, ref.cache_attention(q, cache, table, ints(ctx), cu, window=window), f"window {window}")
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls (shares, and pieces of a chunk) with one workspace, replayed in turn with eager work between."""
+    gen = torch.Generator().manual_seed(94)
+    ctx, d, page = [900, 1500], 64, 64
+    cache, table = filled(gen, ctx, 2, d, page, width=2048)
+    calls = []
+    for new in ([1, 1], [120, 7]):
+        q = torch.randn((sum(new), 8, d), generator=gen).to(BF16).cuda()
+        calls.append((q, None if new == [1, 1] else cu_of(new), torch.empty_like(q)))
+    need = [gdn.cache_attention_workspace_size(q.shape[0], 2, 2048, 8, 2, d, page, cu is not None) for q, cu, _ in calls]
+    assert min(need) > 0
+    ws = torch.empty(max(need), dtype=torch.uint8, device="cuda")
+    want = [gdn.cache_attention(q, cache, table, ints(ctx), cu) for q, cu, _ in calls]
+    lens, graphs = ints(ctx), []
+    torch.cuda.synchronize()
+    for q, cu, out in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            gdn.cache_attention(q, cache, table, lens, cu, out=out, workspace=ws)
+        graphs.append(graph)
+    for turn in range(4):
+        for i in (0, 1) if turn % 2 else (1, 0):
+            calls[i][2].fill_(float("nan"))
+            graphs[i].replay()
+        for i in range(2):
+            assert torch.equal(calls[i][2], want[i]), (turn, i)
+        ws.fill_(0xFF)
+        gdn.cache_attention(calls[0][0], cache, table, lens, None, workspace=ws)
+        torch.cuda.synchronize()
