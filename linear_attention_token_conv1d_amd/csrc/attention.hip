@@ -40,7 +40,7 @@
 // under 24: 364 us, 5.7 TB/s of codes, where a bare read reaches 6.2.
 // 128 rows: bound by the vector instructions that run beside the matrix units
 // (codes to operands, exponentials).  4096 tokens over 8097, the same heads:
-// 611 us, 997 TFLOP/s, where a library product of 8192^3 in bf16 reaches 1128.
+// 616 us, 989 TFLOP/s, where a library product of 8192^3 in bf16 reaches 1128.
 #include "gdn_device.h"
 #include "gdn_internal.h"
 #include "sequences.h"

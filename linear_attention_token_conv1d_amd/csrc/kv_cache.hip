@@ -67,9 +67,41 @@ __device__ __forceinline__ void find_slot(const CacheStoreParams& p, int slot, i
   j = slot - (as_const(p.cu_seqlens)[n] / p.page + 2 * n);
 }
 
-// A code of a page whose scale grows from `was` to `scale`.
-__device__ __forceinline__ uint8_t recode(uint8_t code, float ratio) {
-  return (uint8_t)encode4(__builtin_amdgcn_cvt_f32_fp8((int)code, 0) * ratio, 0.f, 0.f, 0.f);
+// Four codes of a page whose scale grows, by the old scale over the new.
+__device__ __forceinline__ uint32_t recode(uint32_t w, float ratio) {
+  return encode4(__builtin_amdgcn_cvt_f32_fp8((int)w, 0) * ratio, __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * ratio,
+                 __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * ratio, __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * ratio);
+}
+// The codes of a page's first `a` tokens, 16 at a time and four such pieces a thread on their way: in a decode step
+// some page's scale grows nearly always, and the step waits for it (256 sequences, 4 heads of
+// 256, whose pages all do: 31 us, 121 by single codes).  Slots
+// from `a` on keep their bytes: no store covers them.
+template <int THREADS>
+__device__ __forceinline__ void recode_page(uint8_t* codes, int side, int a, int d, int page, float ratio, int tid) {
+  const int pieces = side ? d * page / 16 : a * d / 16, row = page / 16 - 1;  // pieces of a row of values, less one
+  for (int i0 = tid; i0 < pieces; i0 += THREADS * 4) {
+    uint4 w[4];
+    int n[4];  // of the piece's codes that belong to older tokens
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * THREADS;
+      n[j] = i >= pieces ? 0 : side ? min(a - (i & row) * 16, 16) : 16;
+      if (n[j] > 0) w[j] = *reinterpret_cast<const uint4*>(codes + i * 16);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n[j] <= 0) continue;
+      uint8_t* at = codes + (i0 + j * THREADS) * 16;
+      const uint32_t r[4] = {recode(w[j].x, ratio), recode(w[j].y, ratio), recode(w[j].z, ratio), recode(w[j].w, ratio)};
+      if (n[j] == 16) {
+        *reinterpret_cast<uint4*>(at) = make_uint4(r[0], r[1], r[2], r[3]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 15; ++t)
+          if (t < n[j]) at[t] = (uint8_t)(r[t >> 2] >> (8 * (t & 3)));
+      }
+    }
+  }
 }
 
 // x / scale: by its reciprocal where that is exact, which it is for every scale but those that others have set.
@@ -116,18 +148,12 @@ __global__ __launch_bounds__(256) void cache_store_one_kernel(CacheStoreParams p
   most = block_max<64>(most);
   const float scale = page_scale(most, was);
   const Divide by(scale);
-  uint8_t* out = (side ? p.v_cache : p.k_cache) + ((int64_t)pid * p.h_kv + head) * D * p.page + (side ? lane * E * p.page : lane * E);
-  const int step = side ? 1 : D, next = side ? p.page : 1;  // from token to token, from element to element
-  if (a > 0 && scale != was) {
-    const float ratio = was / scale;
-    for (int t = 0; t < a; ++t)
-#pragma unroll
-      for (int e = 0; e < E; ++e) out[t * step + e * next] = recode(out[t * step + e * next], ratio);
-  }
+  uint8_t* codes = (side ? p.v_cache : p.k_cache) + ((int64_t)pid * p.h_kv + head) * D * p.page;
+  if (a > 0 && scale != was) recode_page<64>(codes, side, a, D, p.page, was / scale, lane);
 #pragma unroll
   for (int e = 0; e < E; ++e) f[e] = by(f[e]);
   const uint32_t w = encode4(f[0], E > 1 ? f[E > 1 ? 1 : 0] : 0.f, E > 2 ? f[E > 2 ? 2 : 0] : 0.f, E > 3 ? f[E > 3 ? 3 : 0] : 0.f);
-  uint8_t* at = out + a * step;
+  uint8_t* at = codes + (side ? lane * E * p.page + a : a * D + lane * E);
   if (side) {
 #pragma unroll
     for (int e = 0; e < E; ++e) at[e * p.page] = (uint8_t)(w >> (8 * e));
@@ -222,14 +248,7 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreParams p) {
   const Divide by(scale);
   uint8_t* out = (side ? p.v_cache : p.k_cache) + ((int64_t)pid * p.h_kv + head) * d * p.page;
 
-  if (a > 0 && scale != was) {  // the page's older tokens, by the new scale
-    const float ratio = was / scale;
-    for (int i = tid; i < a * d; i += 256) {
-      const int t = i / d, c = i - t * d;
-      uint8_t* at = out + (side ? c * p.page + t : i);
-      *at = recode(*at, ratio);
-    }
-  }
+  if (a > 0 && scale != was) recode_page<256>(out, side, a, d, p.page, was / scale, tid);
   auto put = [&](int i, const Piece<T>& piece) {
     float f[8];
     uint32_t lo, hi;
