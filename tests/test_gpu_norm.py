@@ -22,6 +22,7 @@ SHAPES = [
     (1, 1, 1, 0), (3, 1, 7, 0), (1, 1, 5120, 0), (5, 48, 128, 2048), (7, 3, 64, 8), (2, 1, 1000, 0), (4, 2, 129, 3),
     (3, 5, 33, 0), (9, 1, 2049, 1), (2, 1, 16384, 0), (2, 1, 16383, 0), (300, 2, 256, 0), (2, 1, 6000, 4), (1000, 1, 8, 0),
     (3, 1, 4096, 0), (2, 1, 8192, 8), (33, 1, 1024, 0), (17, 1, 136, 0), (2, 1, 12288, 0), (3, 1, 520, 0),
+    (3, 1, 4095, 0), (2, 1, 4097, 0), (70, 1, 2500, 1), (2, 4, 136, 3),
 ]
 
 
